@@ -44,27 +44,27 @@ def listed():
     return [
         # one token through a small fp32 top-1 layer with full-probability weights:
         # nothing but latency
-        dict(_few(1, 256, 512, 8, 1, norm=FULLPROB, dtype="fp32"), name="few: 1 token, fp32 top-1"),
+        dict(_few(1, 256, 512, 8, 1, norm=FULLPROB, dtype="fp32"), name="few: 1 token fp32 top-1"),
         # one token of one sequence through a layer of 128 narrow experts with a router bias
-        dict(_few(1, 4096, 1536, 128, 8, bias=True), name="few: 1 token, 128 experts"),
+        dict(_few(1, 4096, 1536, 128, 8, bias=True), name="few: 1 token 128 experts"),
         # a small batch of sequences over eight wide experts: all of them are read
-        dict(_few(7, 4096, 14336, 8, 2), name="few: 7 tokens, wide experts"),
+        dict(_few(7, 4096, 14336, 8, 2), name="few: 7 tokens wide experts"),
         # the largest batch: most of 256 experts, an always-on shared expert, and a capacity limit
-        dict(_few(32, 7168, 2048, 256, 8, d_sh=2048, c=2.0), name="few: 32 tokens, 256 experts"),
+        dict(_few(32, 7168, 2048, 256, 8, d_sh=2048, c=2.0), name="few: 32 tokens 256 experts"),
         # one new token of each of 16 requests, each with an adapter of its own, beside
         # the layer: the adapters' output is added to the layer's
         dict(_adapter(16, 4096, 4096, 64, 16, runs=False), name="adapter: 16 requests"),
         # prompts of up to 32 adapters through a shared projection
-        dict(_adapter(4096, 4096, 4096, 32, 16, W=True, base=False), name="adapter: prompts, projection"),
+        dict(_adapter(4096, 4096, 4096, 32, 16, W=True, base=False), name="adapter: prompts projection"),
         # fp32, a ragged batch whose tokens are in no order, ranks of 40
-        dict(_adapter(1531, 1000, 2056, 7, 40, runs=False, dtype="fp32"), name="adapter: fp32, mixed tokens"),
+        dict(_adapter(1531, 1000, 2056, 7, 40, runs=False, dtype="fp32"), name="adapter: fp32 mixed tokens"),
         # gradients of four adapters beside the layer, long prompts, ranks of 64
         dict(_adapter(8192, 4096, 4096, 4, 64, backward=True), name="adapter grads: beside the layer"),
         # gradients of 16 adapters and of x through a shared projection
         dict(_adapter(2047, 4096, 1536, 16, 16, W=True, base=False, backward=True),
              name="adapter grads: projection"),
         # one decoding-sized batch in fp32: latency
-        dict(_dropout(17, 1024, 0.1, dtype="fp32"), name="dropout: 17 rows, fp32"),
+        dict(_dropout(17, 1024, 0.1, dtype="fp32"), name="dropout: 17 rows fp32"),
         # a training batch, bf16 residual stream
         dict(_dropout(8192, 4096, 0.1), name="dropout: 8192 rows"),
         # the same batch's gradient, as a later shard of the routing group
