@@ -344,6 +344,34 @@ MOE_API moe_status moe_forward(const moe_params* p, const void* x, const void* W
                        moe_stream_t stream);
 
 /*
+ * The whole layer for a few tokens (N <= 32; a decoding step, one token of
+ * each of up to 32 requests), in two kernel launches: the same function as
+ * moe_forward (same arguments, same routing records and statistics, read with
+ * moe_get_stats and moe_workspace_layout), laid out for the time it takes to
+ * read each chosen expert's weights once.  Differences from moe_forward:
+ *   - ws is of moe_few_workspace_size bytes; its first part is laid out as
+ *     moe_workspace_layout says (x_perm, h, h_shared and the rerouting
+ *     candidates are not written, so moe_backward cannot follow);
+ *   - bf16 layers keep h to 16 mantissa bits instead of rounding it to bf16;
+ *   - Y does not depend on the order of any atomics: the same inputs give the
+ *     same bits;
+ *   - the capacity limit and the overflow policies MOE_REJECT_ZERO and
+ *     MOE_REJECT_RENORM are covered; rerouting, acceptance by weight, N > 32
+ *     and E_r > 256 return MOE_ERR_UNSUPPORTED (moe_last_error says which);
+ *   - no stage events.
+ * The second kernel is launched cooperatively (its CTAs, one per SM, meet at a
+ * grid barrier with a bounded wait: MOE_ERR_TIMEOUT from moe_get_stats).  Both
+ * can be captured into a CUDA graph; make the first call on a device outside a
+ * capture.  N = 0 clears the statistics.  Tokens with non-finite scores get no
+ * paths (MOE_ERR_NONFINITE from moe_get_stats), the shared expert still runs.
+ */
+MOE_API moe_status moe_few_workspace_size(const moe_params* p, size_t* bytes);
+MOE_API moe_status moe_forward_few(const moe_params* p, const void* x, const void* W_r, const float* b_r,
+                                   const float* lat, const void* W_g, const void* W_u, const void* W_d,
+                                   const void* Ws_g, const void* Ws_u, const void* Ws_d, float* Y, void* ws,
+                                   moe_stream_t stream);
+
+/*
  * A routing group split over ranks (data parallel: each GPU holds a shard of
  * the group's tokens, ranks in token order, weights replicated).  Capacity
  * competition is defined over the whole routing group ("LLM from scratch"

@@ -20,6 +20,7 @@ __all__ = [
     "moe_workspace_size", "moe_workspace_layout", "moe_route", "moe_dispatch",
     "moe_dispatch_noalloc",
     "moe_expert_ffn", "moe_combine", "moe_forward", "moe_forward_begin", "moe_forward_end",
+    "moe_few_workspace_size", "moe_forward_few",
     "moe_get_stats",
     "moe_set_stage_events", "moe_selftest_wait_timeout", "moe_status_string", "moe_last_error",
     "expert_choice_params", "SoftParams", "soft_params", "moe_soft_workspace_size", "moe_soft_forward",
@@ -118,6 +119,8 @@ def lib():
         L.moe_expert_ffn.argtypes = [pp, _P, _P, _P, _P, _P, _P, _P, _P]
         L.moe_combine.argtypes = [pp, _P, _P, _P, _P, _P, _P]
         L.moe_forward.argtypes = [pp, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]
+        L.moe_few_workspace_size.argtypes = [pp, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_forward_few.argtypes = L.moe_forward.argtypes
         L.moe_get_stats.argtypes = [pp, _P, ctypes.POINTER(Stats), _P]
         L.moe_forward_begin.argtypes = [pp, _P, _P, _P, _P, _P, _P, _P]
         L.moe_forward_end.argtypes = [pp, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
@@ -148,7 +151,8 @@ def lib():
                      "moe_get_stats", "moe_set_stage_events", "moe_forward_begin",
                      "moe_forward_end", "moe_selftest_wait_timeout", "moe_soft_workspace_size",
                      "moe_soft_forward", "moe_soft_check", "moe_dispatch_ranked", "moe_gather_rows",
-                     "moe_backward_workspace_size", "moe_backward", "moe_backward_check"):
+                     "moe_backward_workspace_size", "moe_backward", "moe_backward_check",
+                     "moe_few_workspace_size", "moe_forward_few"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -202,6 +206,30 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+class _on_device_of:
+    """The CUDA device of the tensors, made current for one call (the library
+    launches on the current device and, without a stream, on its current
+    stream); tensors of several devices are refused."""
+
+    def __init__(self, *tensors):
+        index = {t.device.index for t in tensors if hasattr(t, "is_cuda") and t.is_cuda}
+        if len(index) > 1:
+            raise ValueError("libmoe takes tensors of one device; got devices %s" % sorted(index))
+        self.index = index.pop() if index else None
+        self.guard = None
+
+    def __enter__(self):
+        if self.index is not None:
+            import torch
+            if torch.cuda.current_device() != self.index:
+                self.guard = torch.cuda.device(self.index)
+                self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def _check(status: int, where: str):
@@ -268,6 +296,21 @@ def moe_forward(p, x, W_r, b_r, lat, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, Y, ws, str
     _check(lib().moe_forward(ctypes.byref(p), _ptr(x), _ptr(W_r), _ptr(b_r), _ptr(lat), _ptr(W_g),
                              _ptr(W_u), _ptr(W_d), _ptr(Ws_g), _ptr(Ws_u), _ptr(Ws_d), _ptr(Y),
                              _ptr(ws), _stream(stream)), "moe_forward")
+
+
+def moe_few_workspace_size(p: Params) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_few_workspace_size(ctypes.byref(p), ctypes.byref(n)), "moe_few_workspace_size")
+    return n.value
+
+
+def moe_forward_few(p, x, W_r, b_r, lat, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, Y, ws, stream=None):
+    """moe_forward for at most 32 tokens in two launches; ws of
+    moe_few_workspace_size bytes (see moe_forward_few in include/moe.h)."""
+    with _on_device_of(x, W_r, b_r, lat, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, Y, ws):
+        _check(lib().moe_forward_few(ctypes.byref(p), _ptr(x), _ptr(W_r), _ptr(b_r), _ptr(lat), _ptr(W_g),
+                                     _ptr(W_u), _ptr(W_d), _ptr(Ws_g), _ptr(Ws_u), _ptr(Ws_d), _ptr(Y),
+                                     _ptr(ws), _stream(stream)), "moe_forward_few")
 
 
 def moe_forward_begin(p, x, W_r, b_r, lat, counts, ws, stream=None):

@@ -284,6 +284,69 @@ moe_status moe_workspace_size(const moe_params* p, size_t* bytes) {
     return MOE_OK;
 }
 
+static moe_status check_few(const moe_params* p) {
+    moe_status s = check_params(p);
+    if (s != MOE_OK) return s;
+    if (p->N > kFewMaxTokens) {
+        record_error("moe_forward_few: N must be at most 32 (moe_forward takes any N)");
+        return MOE_ERR_UNSUPPORTED;
+    }
+    if (p->E_r > kMaxRouterExperts) {
+        record_error("moe_forward_few: E_r must be at most 256");
+        return MOE_ERR_UNSUPPORTED;
+    }
+    if (p->reject_policy == MOE_REJECT_REROUTE || p->accept_order != MOE_ACCEPT_TOKEN) {
+        record_error("moe_forward_few: rerouting and acceptance by weight are moe_forward's");
+        return MOE_ERR_UNSUPPORTED;
+    }
+    if ((int64_t)p->E_r * p->d_f + p->d_f_shared >= (int64_t)1 << 31) {
+        record_error("moe_forward_few: E_r d_f + d_f_shared must be below 2^31");
+        return MOE_ERR_UNSUPPORTED;
+    }
+    return MOE_OK;
+}
+
+moe_status moe_few_workspace_size(const moe_params* p, size_t* bytes) {
+    moe_status s = check_few(p);
+    if (s != MOE_OK) return s;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    moe_ws_layout L;
+    int n_tiles, tile_tokens;
+    layout(*p, L, n_tiles, tile_tokens);
+    *bytes = few_layout(*p, L.total).total;
+    return MOE_OK;
+}
+
+moe_status moe_forward_few(const moe_params* p, const void* x, const void* W_r, const float* b_r, const float* lat,
+                           const void* W_g, const void* W_u, const void* W_d, const void* Ws_g, const void* Ws_u,
+                           const void* Ws_d, float* Y, void* ws, moe_stream_t stream) {
+    moe_status s = check_few(p);
+    if (s != MOE_OK) return s;
+    if (!ws || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+    const bool sh = p->d_f_shared > 0;
+    if (p->N > 0) {
+        if (!x || !W_r || !W_g || !W_u || !W_d || !Y) return MOE_ERR_INVALID_ARG;
+        if (!aligned16(x) || !aligned16(W_r) || !aligned16(W_g) || !aligned16(W_u) || !aligned16(W_d) || !aligned16(Y))
+            return MOE_ERR_INVALID_ARG;
+        if (p->norm == MOE_NORM_WLR && !lat) return MOE_ERR_INVALID_ARG;
+        if (sh && (!Ws_g || !Ws_u || !Ws_d || !aligned16(Ws_g) || !aligned16(Ws_u) || !aligned16(Ws_d)))
+            return MOE_ERR_INVALID_ARG;
+    }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    WsView v;
+    make_view(*p, ws, v);
+    (void)cudaGetLastError();
+    if (p->N == 0) {
+        cudaError_t e = cudaMemsetAsync(v.counters, 0, CNT_COUNT * 8, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(v.scratch.psum, 0, sizeof(float) * p->E_r, st);
+        return cuda_status(e, "moe_forward_few memset");
+    }
+    const ExpertWeights W{W_g, W_u, W_d, sh ? Ws_g : nullptr, sh ? Ws_u : nullptr, sh ? Ws_d : nullptr};
+    return cuda_status(launch_few(*p, capacity_exact(p->c, p->N, p->k, p->E_r), x, W_r, b_r,
+                                  p->norm == MOE_NORM_WLR ? lat : nullptr, W, Y, v, few_layout(*p, v.lay.total), st),
+                       "moe_forward_few");
+}
+
 moe_status moe_set_stage_events(void* const* events, int n) {
     if (n < 0 || n > 8 || (n > 0 && !events)) return MOE_ERR_INVALID_ARG;
     if (n > 0 && n < 5) return MOE_ERR_INVALID_ARG;

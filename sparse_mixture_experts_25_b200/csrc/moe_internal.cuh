@@ -18,6 +18,7 @@ constexpr int kMaxRouterExperts = 256;  // E_r limit of the fused router kernel
 constexpr int kMaxK = 32;             // k limit (warp-wide selection)
 constexpr int kTcBM = 128;            // M tile of the tcgen05 grouped GEMM
 constexpr int kSimtBM = 64;           // M tile of the fp32 grouped GEMM
+constexpr int kFewMaxTokens = 32;     // N limit of the few-token layer (one bit per token)
 
 // indices into the int64 device counter block (moe_ws_layout.counters)
 enum Counter {
@@ -213,6 +214,19 @@ cudaError_t launch_simt_down(const moe_params& p, int mode, const void* h, const
                              const int32_t* offsets, const int32_t* mt_start,
                              const ExpertWeights& W, const int32_t* slot_token,
                              const float* slot_w, float* Y, float* H_out, cudaStream_t st);
+
+// few.cu: the whole layer for at most kFewMaxTokens tokens.  Its part of the
+// workspace follows the layer's own regions.
+struct FewLayout {
+    size_t bar;   // grid barrier
+    size_t part;  // partial router scores
+    size_t h;     // hidden activations
+    size_t total;
+};
+FewLayout few_layout(const moe_params& p, size_t after);
+cudaError_t launch_few(const moe_params& p, int64_t C, const void* x, const void* W_r, const float* b_r,
+                       const float* lat, const ExpertWeights& W, float* Y, const WsView& v, const FewLayout& L,
+                       cudaStream_t st);
 
 int num_sms();
 
