@@ -356,8 +356,9 @@ MOE_API moe_status moe_forward(const moe_params* p, const void* x, const void* W
  *   - Y does not depend on the order of any atomics: the same inputs give the
  *     same bits;
  *   - the capacity limit and the overflow policies MOE_REJECT_ZERO and
- *     MOE_REJECT_RENORM are covered; rerouting, acceptance by weight, N > 32
- *     and E_r > 256 return MOE_ERR_UNSUPPORTED (moe_last_error says which);
+ *     MOE_REJECT_RENORM are covered; rerouting, acceptance by weight, N > 32,
+ *     E_r > 256 and E_r d_f + d_f_shared or d of 2^24 and more return
+ *     MOE_ERR_UNSUPPORTED (moe_last_error says which);
  *   - no stage events.
  * The second kernel is launched cooperatively (its CTAs, one per SM, meet at a
  * grid barrier with a bounded wait: MOE_ERR_TIMEOUT from moe_get_stats).  Both

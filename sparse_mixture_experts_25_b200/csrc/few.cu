@@ -15,14 +15,18 @@
 //                      of the gate/up rows, meets the others at one grid
 //                      barrier (h is complete), and streams its share of the
 //                      down rows.
-// The work is cut by weight ROWS, so every CTA reads the same number of bytes
-// to within one row whatever the sizes: CTA c of G takes hidden units
-// [c T / G, (c+1) T / G) of the T = sum d_f units of the chosen (and shared)
-// experts, then output features [c d / G, (c+1) d / G) of every expert.
-// A producer warp copies rows with bulk copies into a ring of stages of 16
-// rows x 2 KB and runs ahead across tiles, experts and the grid barrier (the
-// down weights do not depend on h), so the memory stays busy while the other
-// warps reduce and wait.
+// The work is cut by weight ROWS, so the CTAs finish together whatever the
+// sizes: CTA c of G takes its share of the hidden units of all chosen (and
+// shared) experts, each weighted by what its expert's stages cost, then output
+// features [c d / G, (c+1) d / G) of every expert.
+// Producer warps copy pieces of up to 2 KB of 16 weight rows, and of the
+// tokens' rows that they meet, into a ring of stages with bulk copies.  They
+// run ahead across tiles and experts, and fill the ring with down weights
+// before the grid barrier (only the rows of h wait for it), so the memory stays
+// busy while the other warps reduce and wait.  There are four of them because a
+// warp takes about 32 ns to issue a copy: on rings that are only emptied, 16
+// rows of 1 KB a stage reach 4.0 TB/s with one producer warp, 6.2 with two and
+// 7.3 with four.
 //
 // bf16: mma.sync m16n8k16 with the 16 weight rows as M and the tokens as N;
 // the eight consumer warps take K steps of 32 in turn and their partial sums
@@ -41,18 +45,16 @@
 #include "router_select.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace {
 
 constexpr int kFewConsumers = 8;                     // consumer warps
-constexpr int kFewThreads = 32 * (kFewConsumers + 1);
+constexpr int kFewProducers = 4;                     // producer warps
+constexpr int kFewThreads = 32 * (kFewConsumers + kFewProducers);
 constexpr int kFewRows = 16;                         // weight rows of a stage
-constexpr int kFewChunk = 2048;                      // bytes of a row in a stage
-// 64 bytes of padding put two consecutive rows on different halves of the
-// banks, so a quarter-warp's 16-byte reads (2 rows x 64 bytes) do not collide
-constexpr int kFewPitch = kFewChunk + 64;
-constexpr int kFewStage = kFewRows * kFewPitch;
+constexpr int kFewChunk = 2048;                      // most bytes of a row in a stage
 constexpr int kFewMaxPaths = kFewMaxTokens * kMaxK;
 
 struct FewArgs {
@@ -98,10 +100,12 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // two MMAs over the 32 K elements of a step: each lane's 8 elements of its
-// rows (lo: row g, hi: row g + 8) against 8 elements of column g
-__device__ __forceinline__ void mma_step(float (&c)[4], const uint4& lo, const uint4& hi, const uint4& b) {
+// rows (lo: row g, hi: row g + 8) against 8 elements of column g.  They sum
+// into two accumulators, so that neither waits for the other
+__device__ __forceinline__ void mma_step(float (&c)[4], float (&d)[4], const uint4& lo, const uint4& hi,
+                                         const uint4& b) {
     mma_bf16(c, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-    mma_bf16(c, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+    mma_bf16(d, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
 }
 
 // ---------------------------------------------------------------------------
@@ -114,6 +118,7 @@ __global__ void __launch_bounds__(256)
     few_scores_kernel(const void* xv, const void* wv, int N, int d, int E, int slice, float* part, unsigned* bar,
                       unsigned long long* counters) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the layer's CTAs may get ready
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         if (tid == 0) *bar = 0u;
         if (tid < CNT_COUNT) counters[tid] = 0ull;
@@ -127,7 +132,7 @@ __global__ void __launch_bounds__(256)
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(xv);
         const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(wv);
         const bool two = N > 16;
-        float acc[2][4] = {};
+        float acc[4][4] = {};
         const __nv_bfloat16* wr = e0 + g < E ? w + (int64_t)(e0 + g) * d : nullptr;
         const uint4 zero = make_uint4(0, 0, 0, 0);
         auto ld = [&](const __nv_bfloat16* row, int k, bool ok) {
@@ -139,19 +144,19 @@ __global__ void __launch_bounds__(256)
             const uint4 b = ld(wr, k, in && wr);
             const uint4 a0 = ld(x + (int64_t)g * d, k, in && g < N);
             const uint4 a1 = ld(x + (int64_t)(g + 8) * d, k, in && g + 8 < N);
-            mma_step(acc[0], a0, a1, b);
+            mma_step(acc[0], acc[2], a0, a1, b);
             if (two) {
                 const uint4 a2 = ld(x + (int64_t)(g + 16) * d, k, in && g + 16 < N);
                 const uint4 a3 = ld(x + (int64_t)(g + 24) * d, k, in && g + 24 < N);
-                mma_step(acc[1], a2, a3, b);
+                mma_step(acc[1], acc[3], a2, a3, b);
             }
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            red[warp][m * 16 + g][2 * t] = acc[m][0];
-            red[warp][m * 16 + g][2 * t + 1] = acc[m][1];
-            red[warp][m * 16 + g + 8][2 * t] = acc[m][2];
-            red[warp][m * 16 + g + 8][2 * t + 1] = acc[m][3];
+            red[warp][m * 16 + g][2 * t] = acc[m][0] + acc[m + 2][0];
+            red[warp][m * 16 + g][2 * t + 1] = acc[m][1] + acc[m + 2][1];
+            red[warp][m * 16 + g + 8][2 * t] = acc[m][2] + acc[m + 2][2];
+            red[warp][m * 16 + g + 8][2 * t + 1] = acc[m][3] + acc[m + 2][3];
         }
         __syncthreads();
         const int tok = tid >> 3, e = e0 + (tid & 7);
@@ -191,6 +196,17 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------------------
 // The layer
 // ---------------------------------------------------------------------------
+// An expert with rows (or the shared one, last): its weight matrices' row
+// block, its rows of h, and how its rows are cut into stages
+struct FewGroup {
+    int e;               // expert, 0 for the shared one
+    int row0, R;         // first row (h, row_tok, row_w) and number of rows
+    int F;               // hidden units
+    int len1, pitch1;    // gate/up pieces (rows of d)
+    int len2, pitch2;    // down pieces (rows of F)
+    int unit_cost;       // relative cost of a gate/up unit
+};
+
 struct FewShared {
     int32_t ids[kFewMaxPaths];
     float w[kFewMaxPaths];
@@ -199,20 +215,24 @@ struct FewShared {
     uint32_t asked[kMaxRouterExperts];   // tokens that asked for expert e, one bit each
     uint32_t taken[kMaxRouterExperts];   // tokens it accepted
     int32_t base[kMaxRouterExperts + 1]; // first row of expert e
-    int32_t act[kMaxRouterExperts + 1];  // experts with rows, in order
+    FewGroup grp[kMaxRouterExperts + 1]; // experts with rows, in order, then the shared one
+    uint32_t cost[kMaxRouterExperts + 2]; // cost of the gate/up units of the groups before
     uint8_t row_tok[kFewMaxPaths];
     float row_w[kFewMaxPaths];
     unsigned long long counters[CNT_COUNT];
-    int n_act, n_rows;
+    int warp_rows[8], warp_n[8];         // rows and experts with rows among each 32 experts
+    int from[2], to[2];                  // this CTA's units: group and unit, from and to
     int abort_flag;
 };
 
-constexpr int few_stages(int NT) { return NT == 4 ? 4 : 5; }
-constexpr size_t few_red_bytes(bool bf16, int NT) { return bf16 ? 2 * 8 * (size_t)NT * 128 * 4 : 0; }
-constexpr size_t few_yacc_bytes(bool bf16, int NT) { return (bf16 ? 8 : 1) * (size_t)NT * 8 * kFewRows * 4; }
+// stages of the ring and their size: the rest of the shared memory holds the
+// reductions, which grow with the token tiles NT
+constexpr int few_stages(int) { return 4; }
+constexpr int few_stage_bytes(int NT) { return NT == 1 ? 46 * 1024 : (NT == 2 ? 44 * 1024 : 40 * 1024); }
+// gate/up: partial sums of 8 warps, two buffers; down: 8 warps' sums per token (fp32: one)
+constexpr size_t few_red_bytes(bool bf16, int NT) { return (bf16 ? 2 * 8 * 128 * 4 : 8 * kFewRows * 4) * (size_t)NT; }
 constexpr size_t few_smem(bool bf16, int NT) {
-    return few_stages(NT) * (size_t)kFewStage + few_red_bytes(bf16, NT) + few_yacc_bytes(bf16, NT) + 128 +
-           sizeof(FewShared);
+    return few_stages(NT) * (size_t)few_stage_bytes(NT) + few_red_bytes(bf16, NT) + 128 + sizeof(FewShared);
 }
 
 // a stage position in the ring
@@ -227,17 +247,16 @@ struct RingPos {
     }
 };
 
-// elements of one row that a stage holds: the row in equal pieces of at most
-// kFewChunk bytes, multiples of 32 elements
-__device__ __forceinline__ int few_chunk(int K, int es) {
-    const int n = (int)(((int64_t)K * es + kFewChunk - 1) / kFewChunk);
-    return ((K + n - 1) / n + 31) / 32 * 32;
-}
-
-// the share [lo, hi) of `total` items of this CTA
-__device__ __forceinline__ void few_share(int64_t total, int& lo, int& hi) {
-    lo = (int)(total * blockIdx.x / gridDim.x);
-    hi = (int)(total * (blockIdx.x + 1) / gridDim.x);
+// How rows of K elements are cut when a stage holds `rows` of them: `len`
+// elements a piece (equal pieces, multiples of 32 elements), rows `pitch` bytes
+// apart.  The pitch is 64 bytes above a multiple of 128, which puts two
+// consecutive rows on different halves of the banks, so a quarter-warp's
+// 16-byte reads (2 rows x 64 bytes) do not collide.
+__device__ __forceinline__ void few_cut(int K, int es, int rows, int stage_bytes, int& len, int& pitch) {
+    const int cap = min(kFewChunk, (stage_bytes / rows - 64) & ~127) / es;  // elements, a multiple of 32
+    const int n = (K + cap - 1) / cap;
+    len = ((K + n - 1) / n + 31) / 32 * 32;
+    pitch = cap * es + 64;
 }
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -245,16 +264,19 @@ __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;
 template <bool BF16, int NT>
 __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_constant__ FewArgs a) {
     constexpr int ST = few_stages(NT);
+    constexpr int SB = few_stage_bytes(NT);
     constexpr int ES = BF16 ? 2 : 4;
+    constexpr int PL = BF16 ? 2 : 1;  // parts that h is kept in
+    static_assert(SB / (kFewRows + PL * NT * 8) >= 128 + 64, "a stage holds a piece of every row");
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;
-    float* red = reinterpret_cast<float*>(smem + ST * kFewStage);
-    float* yacc = reinterpret_cast<float*>(smem + ST * kFewStage + few_red_bytes(BF16, NT));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + ST * kFewStage + few_red_bytes(BF16, NT) +
-                                                 few_yacc_bytes(BF16, NT));
+    float* red = reinterpret_cast<float*>(smem + ST * SB);
+    float* yacc = red;  // gate/up is over when the down sums begin
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + ST * SB + few_red_bytes(BF16, NT));
     uint64_t* empty = full + ST;
+    uint64_t* h_ready = empty + ST;
     FewShared& S = *reinterpret_cast<FewShared*>(reinterpret_cast<uint8_t*>(full) + 128);
-    static_assert(2 * ST * 8 <= 128, "barriers");
+    static_assert((2 * ST + 1) * 8 <= 128, "barriers");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort_flag = &S.abort_flag;
 
@@ -266,12 +288,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     if (tid < CNT_COUNT) S.counters[tid] = 0ull;
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], kFewProducers);
             mbar_init(&empty[s], kFewConsumers);
         }
+        mbar_init(h_ready, 1);
         S.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    // launched while the scores kernel runs: its results count from here on
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
     {
         RouterArgs r = a.sel;
@@ -280,21 +305,39 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         r.margin = S.margin;
         r.counters = S.counters;
         float* ps = blockIdx.x == 0 ? S.psum : nullptr;  // only one CTA writes the records
+        // scores: the K slices' sums in order, in the ring's memory
+        float* g = reinterpret_cast<float*>(ring);
+        const int ne = a.N * a.E;
+        if (a.E % 4 == 0) {
+#pragma unroll 2
+            for (int i = tid * 4; i < ne; i += kFewThreads * 4) {
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int q = 0; q < a.KS; ++q) {
+                    const float4 v = *reinterpret_cast<const float4*>(a.part + (int64_t)q * ne + i);
+                    s.x += v.x;
+                    s.y += v.y;
+                    s.z += v.z;
+                    s.w += v.w;
+                }
+                *reinterpret_cast<float4*>(g + i) = s;
+            }
+        } else {
+            for (int i = tid; i < ne; i += kFewThreads) {
+                float s = 0.f;
+#pragma unroll 4
+                for (int q = 0; q < a.KS; ++q) s += a.part[(int64_t)q * ne + i];
+                g[i] = s;
+            }
+        }
+        __syncthreads();
         auto load = [&](int t, int e) {
-            if (e >= a.E) return -INFINITY;
-            float s = 0.f;
-            for (int q = 0; q < a.KS; ++q) s += a.part[((int64_t)q * a.N + t) * a.E + e];
-            return a.sel.b_r ? s + a.sel.b_r[e] : s;
+            return e < a.E ? g[t * a.E + e] + (a.sel.b_r ? a.sel.b_r[e] : 0.f) : -INFINITY;
         };
-        for (int t = warp; t < a.N; t += kFewConsumers + 1) {
+        for (int t = warp; t < a.N; t += kFewThreads / 32) {
             if (a.E <= 32) {
                 float v[1] = {load(t, lane)};
                 select_token<1>(r, t, lane, v, ps);
-            } else if (a.E <= 128) {
-                float v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = load(t, lane + 32 * i);
-                select_token<4>(r, t, lane, v, ps);
             } else {
                 float v[8];
 #pragma unroll
@@ -303,374 +346,248 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             }
         }
     }
+    fence_async_smem();  // the ring's memory is the copies' from here on
     __syncthreads();
     const int paths = a.N * a.k;
     for (int i = tid; i < paths; i += kFewThreads)
         if (S.ids[i] >= 0) atomicOr(&S.asked[S.ids[i]], 1u << (i / a.k));
     __syncthreads();
-    for (int e = tid; e < a.E; e += kFewThreads) {
-        uint32_t m = S.asked[e];
+    // accepted tokens, rows and groups: a warp for every 32 experts
+    int e_rows = 0, e_at = 0, e_n = 0;
+    unsigned e_have = 0;
+    if (warp < 8) {
+        const int e = tid;
+        uint32_t m = e < a.E ? S.asked[e] : 0u;
         for (int over = __popc(m) - a.C; over > 0; --over) m &= ~(0x80000000u >> __clz(m));  // the first C stay
-        S.taken[e] = m;
+        if (e < a.E) S.taken[e] = m;
+        e_rows = __popc(m);
+        e_at = e_rows;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, e_at, o);
+            if (lane >= o) e_at += u;
+        }
+        e_have = __ballot_sync(0xffffffffu, e_rows > 0);
+        if (lane == 31) S.warp_rows[warp] = e_at;
+        if (lane == 0) S.warp_n[warp] = __popc(e_have);
+        e_at -= e_rows;
+    }
+    __syncthreads();
+    int n_rows = 0, n_act = 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        if (q == warp) {
+            e_at += n_rows;
+            e_n = n_act;
+        }
+        n_rows += S.warp_rows[q];
+        n_act += S.warp_n[q];
+    }
+    const int n_groups = n_act + (a.d_sh > 0 ? 1 : 0);
+    if (warp < 8 && tid < a.E) S.base[tid] = e_at;
+    const bool own = warp < 8 && e_rows > 0, shared = tid == kFewThreads - 1 && a.d_sh > 0;
+    if (own || shared) {
+        FewGroup gr;
+        gr.e = own ? tid : 0;
+        gr.row0 = own ? e_at : n_rows;
+        gr.R = own ? e_rows : a.N;
+        gr.F = own ? a.d_f : a.d_sh;
+        few_cut(a.d, ES, kFewRows + gr.R, SB, gr.len1, gr.pitch1);
+        few_cut(gr.F, ES, kFewRows + PL * gr.R, SB, gr.len2, gr.pitch2);
+        // a unit's cost: its stages' bytes at an SM's share of the memory (47
+        // bytes/ns) or the issue of their copies (15 ns each), whichever is
+        // longer, in 1/16 of the first (at most 255)
+        const int n = (a.d + gr.len1 - 1) / gr.len1;
+        const int mem = a.d * (kFewRows * ES) / 47 + 1, issue = n * (kFewRows + gr.R) * 15;
+        gr.unit_cost = issue > mem ? min(255, (int)(issue * 16ll / mem)) : 16;
+        const int at = own ? e_n + __popc(e_have & ((1u << lane) - 1u)) : n_act;
+        S.grp[at] = gr;
+        S.cost[at + 1] = (uint32_t)gr.unit_cost * gr.F;
+    }
+    if (tid == 0) {
+        S.base[a.E] = n_rows;
+        S.cost[0] = 0;
     }
     __syncthreads();
     if (warp == 0) {
-        int rows = 0, n = 0;
-        for (int b = 0; b < a.E; b += 32) {
-            const int e = b + lane;
-            const int c = e < a.E ? __popc(S.taken[e]) : 0;
-            int v = c;
+        // this CTA's share of the gate/up units, as a span of (group, unit)
+        uint32_t sum = 0;
+        for (int b = 0; b < n_groups; b += 32) {
+            const int i = b + lane;
+            uint32_t v = i < n_groups ? S.cost[i + 1] : 0u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += u;
             }
-            if (e < a.E) S.base[e] = rows + v - c;
-            const unsigned have = __ballot_sync(0xffffffffu, c > 0);
-            if (c > 0) S.act[n + __popc(have & ((1u << lane) - 1u))] = e;
-            rows += __shfl_sync(0xffffffffu, v, 31);
-            n += __popc(have);
+            if (i < n_groups) S.cost[i + 1] = sum + v;
+            sum += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) {
-            S.base[a.E] = rows;
-            S.n_rows = rows;
-            S.n_act = n;
-        }
-    }
-    __syncthreads();
-    for (int i = tid; i < paths; i += kFewThreads) {
-        const int e = S.ids[i], t = i / a.k;
-        if (e < 0 || !((S.taken[e] >> t) & 1u)) continue;
-        const int r = S.base[e] + __popc(S.taken[e] & ((1u << t) - 1u));
-        float wc = S.w[i];
-        if (a.reject == MOE_REJECT_RENORM) {  // a token that lost a path shares its weight out again
-            float sum = 0.f;
-            bool lost = false;
-            for (int j = t * a.k; j < (t + 1) * a.k; ++j) {
-                const int f = S.ids[j];
-                if (f < 0) continue;
-                if ((S.taken[f] >> t) & 1u) sum += S.w[j];
-                else lost = true;
+        __syncwarp();
+        if (lane < 2) {
+            const uint32_t c = blockIdx.x + lane, q = sum / gridDim.x, at = q * c + (sum - q * gridDim.x) * c / gridDim.x;
+            int lo = 0, hi = n_groups;  // the last group that begins at or before `at` (n_groups at the end)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (S.cost[mid] <= at) lo = mid;
+                else hi = mid - 1;
             }
-            if (lost && sum > 0.f) wc = wc / sum;
-        }
-        S.row_tok[r] = (uint8_t)t;
-        S.row_w[r] = wc;
-    }
-    __syncthreads();
-
-    const int n_act = S.n_act, n_rows = S.n_rows;
-    const int n_groups = n_act + (a.d_sh > 0 ? 1 : 0);
-    int u0, u1, c0, c1;
-    few_share((int64_t)n_act * a.d_f + a.d_sh, u0, u1);
-    few_share(a.d, c0, c1);
-    // tile at unit u: the group, its first unit, and how many (at most 8, inside the group and the share)
-    auto unit_tile = [&](int u, int& gi, int& j, int& nj) {
-        gi = u < n_act * a.d_f ? u / a.d_f : n_act;
-        j = u - gi * a.d_f;
-        nj = min(min(8, (gi < n_act ? a.d_f : a.d_sh) - j), u1 - u);
-    };
-
-    if (warp == kFewConsumers) {
-        // ---- producer ----
-        RingPos pos;
-        int used = 0;  // stages filled at least once
-        bool ok = true;
-        auto fill = [&](int rows, const uint8_t* src, uint32_t bytes, int row_slot) {
-            // lanes 0 .. rows - 1 copy their row; src is this lane's
-            if (!warp_wait_bounded(&empty[pos.stage], pos.phase ^ 1u, abort_flag, a.counters)) return false;
-            if (lane == 0) mbar_expect_tx(&full[pos.stage], rows * bytes);
-            __syncwarp();
-            if (lane < rows)
-                bulk_load(smem_u32(ring) + pos.stage * kFewStage + row_slot * kFewPitch, src, bytes,
-                          &full[pos.stage]);
-            if (used < ST) ++used;
-            pos.next(ST);
-            return true;
-        };
-        const int lenA = few_chunk(a.d, ES);
-        for (int u = u0; u < u1 && ok;) {
-            int gi, j, nj;
-            unit_tile(u, gi, j, nj);
-            const bool up = lane >= nj;
-            const int jj = j + (up ? lane - nj : lane);
-            const uint8_t* W = static_cast<const uint8_t*>(gi < n_act ? (up ? a.W_u : a.W_g) : (up ? a.Ws_u : a.Ws_g));
-            const int64_t row = (gi < n_act ? (int64_t)S.act[gi] * a.d_f : 0) + jj;
-            const uint8_t* src = W + row * a.d * ES;
-            for (int kb = 0; kb < a.d && ok; kb += lenA)
-                ok = fill(2 * nj, src + (int64_t)kb * ES, (uint32_t)(min(lenA, a.d - kb) * ES), up ? 8 + lane - nj : lane);
-            u += nj;
-        }
-        for (int c = c0; c < c1 && ok; c += kFewRows) {
-            const int nc = min(kFewRows, c1 - c);
-            for (int gi = 0; gi < n_groups && ok; ++gi) {
-                const int K = gi < n_act ? a.d_f : a.d_sh;
-                const int len = few_chunk(K, ES);
-                const uint8_t* W = static_cast<const uint8_t*>(gi < n_act ? a.W_d : a.Ws_d);
-                const int64_t row = (gi < n_act ? (int64_t)S.act[gi] * a.d : 0) + c + lane;
-                const uint8_t* src = W + row * K * ES;
-                for (int kb = 0; kb < K && ok; kb += len)
-                    ok = fill(nc, src + (int64_t)kb * ES, (uint32_t)(min(len, K - kb) * ES), lane);
-            }
-        }
-        // every copy has landed before the CTA may leave, also when a wait
-        // gave up: the last fill of each used stage, with a limit
-        const unsigned long long t0 = global_timer_ns();
-        for (int s = 0; s < used; ++s) {
-            const uint32_t par = s < pos.stage ? pos.phase : pos.phase ^ 1u;
-            while (!mbar_try_wait(smem_u32(&full[s]), par) && global_timer_ns() - t0 < kTimeoutNs) {
-            }
+            int* out = lane ? S.to : S.from;
+            out[0] = lo;
+            out[1] = lo < n_groups ? (int)((at - S.cost[lo]) / (uint32_t)S.grp[lo].unit_cost) : 0;
         }
     } else {
-        // ---- consumers ----
+        for (int i = tid - 32; i < paths; i += kFewThreads - 32) {
+            const int e = S.ids[i], t = i / a.k;
+            if (e < 0 || !((S.taken[e] >> t) & 1u)) continue;
+            const int r = S.base[e] + __popc(S.taken[e] & ((1u << t) - 1u));
+            float wc = S.w[i];
+            if (a.reject == MOE_REJECT_RENORM) {  // a token that lost a path shares its weight out again
+                float sum = 0.f;
+                bool lost = false;
+                for (int j = t * a.k; j < (t + 1) * a.k; ++j) {
+                    const int f = S.ids[j];
+                    if (f < 0) continue;
+                    if ((S.taken[f] >> t) & 1u) sum += S.w[j];
+                    else lost = true;
+                }
+                if (lost && sum > 0.f) wc = wc / sum;
+            }
+            S.row_tok[r] = (uint8_t)t;
+            S.row_w[r] = wc;
+        }
+    }
+    __syncthreads();
+    const int g_to = S.to[0], j_to = S.to[1];
+    // the next tile of at most 8 units of a group, from (gi, j) on; false at the end of the share
+    auto unit_tile = [&](int& gi, int& j, int& nj) {
+        if (gi < n_groups && j >= S.grp[gi].F) {
+            ++gi;
+            j = 0;
+        }
+        if (gi > g_to || (gi == g_to && j >= j_to)) return false;
+        nj = min(8, (gi == g_to ? j_to : S.grp[gi].F) - j);
+        return true;
+    };
+    // the output features go in equal tiles of at most 16
+    const int c0 = (int)((int64_t)a.d * blockIdx.x / gridDim.x), c1 = (int)((int64_t)a.d * (blockIdx.x + 1) / gridDim.x);
+    const int c_tiles = (c1 - c0 + kFewRows - 1) / kFewRows;
+    const int c_rows = c_tiles ? (c1 - c0 + c_tiles - 1) / c_tiles : 1;
+
+    if (warp >= kFewConsumers) {
+        // ---- producers: row i of a stage is copied by lane i / 4 of warp i % 4 ----
+        const int mine = lane * kFewProducers + warp - kFewConsumers;
+        static_assert(kFewRows + 2 * kFewMaxTokens <= 32 * kFewProducers, "a lane for every row of a stage");
         RingPos pos;
-        const int g = lane >> 2, t = lane & 3;
-        const uint4 zero4 = make_uint4(0, 0, 0, 0);
-        // bf16: one group's rows (16 weight rows against `ntr` column tiles),
-        // summed over K; `ptr` the columns' rows (null: no such column)
-        auto mma_rows = [&](int K, const __nv_bfloat16* const (&ptr)[NT], int planes, int64_t plane, int ntr,
-                            float (&acc)[NT][4]) {
-            constexpr int PF = NT == 1 ? 4 : (NT == 2 ? 2 : 1);
-            const int len0 = few_chunk(K, 2);
-            for (int kb = 0; kb < K; kb += len0) {
-                const int len = min(len0, K - kb);
-                const int steps = (len + 31) / 32;
-                const uint8_t* st = ring + pos.stage * kFewStage;
-                bool waited = false, ok = true;
-                for (int s0 = warp; s0 < steps || !waited; s0 += kFewConsumers * PF) {
-                    // the columns' operands first: their latency passes while the rows arrive
-                    uint4 b[PF][2][NT];
-#pragma unroll
-                    for (int p = 0; p < PF; ++p) {
-                        const int kk = (s0 + p * kFewConsumers) * 32 + t * 8;
-#pragma unroll
-                        for (int pl = 0; pl < 2; ++pl)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                b[p][pl][n] = (kk < len && ptr[n] && pl < planes)
-                                                  ? *reinterpret_cast<const uint4*>(ptr[n] + pl * plane + kb + kk)
-                                                  : zero4;
-                    }
-                    if (!waited) {
-                        ok = warp_wait_bounded(&full[pos.stage], pos.phase, abort_flag, a.counters);
-                        waited = true;
-                    }
-                    if (!ok) break;
-#pragma unroll
-                    for (int p = 0; p < PF; ++p) {
-                        const int s = s0 + p * kFewConsumers;
-                        if (s >= steps) break;
-                        const int kk = s * 32 + t * 8;
-                        uint4 lo = zero4, hi = zero4;
-                        if (kk < len) {  // what lies behind a row's end in the stage is not a number to use
-                            lo = *reinterpret_cast<const uint4*>(st + g * kFewPitch + kk * 2);
-                            hi = *reinterpret_cast<const uint4*>(st + (g + 8) * kFewPitch + kk * 2);
-                        }
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if (n < ntr) {
-                                mma_step(acc[n], lo, hi, b[p][0][n]);
-                                if (planes > 1) mma_step(acc[n], lo, hi, b[p][1][n]);
-                            }
-                        }
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[pos.stage]);
-                pos.next(ST);
-            }
+        int used = 0;  // stages filled at least once
+        // takes the next stage, which this warp copies `rows` pieces of `bytes` to
+        auto open = [&](int rows, uint32_t bytes) {
+            if (!warp_wait_bounded(&empty[pos.stage], pos.phase ^ 1u, abort_flag, a.counters)) return false;
+            if (lane == 0)
+                mbar_expect_tx(&full[pos.stage],
+                               (rows + kFewProducers - 1 - (warp - kFewConsumers)) / kFewProducers * bytes);
+            __syncwarp();
+            if (used < ST) ++used;
+            return true;
         };
-        // fp32: rows `warp` and `warp + 8` of the stage against R columns
-        auto ffma_rows = [&](int K, const float* x, int64_t ldx, const uint8_t* tok, int R, float (&acc)[2][NT * 8]) {
-            const int len0 = few_chunk(K, 4);
-            for (int kb = 0; kb < K; kb += len0) {
-                const int len = min(len0, K - kb);
-                const uint8_t* st = ring + pos.stage * kFewStage;
-                if (warp_wait_bounded(&full[pos.stage], pos.phase, abort_flag, a.counters)) {
-                    for (int kk = lane * 4; kk < len; kk += 128) {
-                        const float4 p = *reinterpret_cast<const float4*>(st + warp * kFewPitch + kk * 4);
-                        const float4 q = *reinterpret_cast<const float4*>(st + (warp + 8) * kFewPitch + kk * 4);
-#pragma unroll
-                        for (int r = 0; r < NT * 8; ++r) {
-                            if (r < R) {
-                                const int row = tok ? tok[r] : r;
-                                const float4 v = *reinterpret_cast<const float4*>(x + row * ldx + kb + kk);
-                                acc[0][r] += p.x * v.x + p.y * v.y + p.z * v.z + p.w * v.w;
-                                acc[1][r] += q.x * v.x + q.y * v.y + q.z * v.z + q.w * v.w;
-                            }
-                        }
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[pos.stage]);
-                pos.next(ST);
-            }
+        auto copy = [&](int stage, int slot, int pitch, const uint8_t* src, uint32_t bytes) {
+            bulk_load(smem_u32(ring) + stage * SB + slot * pitch, src, bytes, &full[stage]);
         };
-
-        // gate/up: h of this CTA's hidden units
-        int tile = 0;
-        for (int u = u0; u < u1; ++tile) {
-            int gi, j, nj;
-            unit_tile(u, gi, j, nj);
-            const bool routed = gi < n_act;
-            const int e = routed ? S.act[gi] : 0;
-            const int row0 = routed ? S.base[e] : n_rows;
-            const int R = routed ? __popc(S.taken[e]) : a.N;
-            const uint8_t* tok = routed ? S.row_tok + row0 : nullptr;
-            if constexpr (BF16) {
-                const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
-                const __nv_bfloat16* ptr[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int r = n * 8 + g;
-                    ptr[n] = r < R ? x + (int64_t)(tok ? tok[r] : r) * a.d : nullptr;
+        auto gate_up = [&]() {
+            int nj;
+            for (int gi = S.from[0], j = S.from[1]; unit_tile(gi, j, nj); j += nj) {
+                const FewGroup gr = S.grp[gi];
+                const int rows = 2 * nj + gr.R;
+                // this lane's row: a gate row, an up row or a token's row
+                const uint8_t* src = nullptr;
+                int slot = 0;
+                if (mine < 2 * nj) {
+                    const bool up = mine >= nj;
+                    const int jj = up ? mine - nj : mine;
+                    const void* m = gi < n_act ? (up ? a.W_u : a.W_g) : (up ? a.Ws_u : a.Ws_g);
+                    src = static_cast<const uint8_t*>(m) + ((int64_t)gr.e * a.d_f + j + jj) * a.d * ES;
+                    slot = (up ? 8 : 0) + jj;
+                } else if (mine < rows) {
+                    const int r = mine - 2 * nj;
+                    const int tok = gi < n_act ? S.row_tok[gr.row0 + r] : r;
+                    src = static_cast<const uint8_t*>(a.x) + (int64_t)tok * a.d * ES;
+                    slot = kFewRows + r;
                 }
-                float acc[NT][4] = {};
-                const int ntr = (R + 7) / 8;
-                mma_rows(a.d, ptr, 1, 0, ntr, acc);
-                // warps' partial sums: [n][16 rows][8 columns], two buffers in turn
-                float* mine = red + ((tile & 1) * 8 + warp) * (NT * 128);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    *reinterpret_cast<float2*>(mine + n * 128 + g * 8 + 2 * t) = make_float2(acc[n][0], acc[n][1]);
-                    *reinterpret_cast<float2*>(mine + n * 128 + (g + 8) * 8 + 2 * t) = make_float2(acc[n][2], acc[n][3]);
-                }
-                consumer_sync();
-                const int unit = tid & 7, r = tid >> 3;
-                if (r < R && unit < nj) {
-                    const float* p = red + (tile & 1) * 8 * (NT * 128) + (r >> 3) * 128 + unit * 8 + (r & 7);
-                    float zg = 0.f, zu = 0.f;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        zg += p[q * (NT * 128)];
-                        zu += p[q * (NT * 128) + 64];
-                    }
-                    const float hv = zg / (1.0f + expf(-zg)) * zu;
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(hv);
-                    __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.h) + (int64_t)(row0 + r) * a.ldh + j + unit;
-                    h[0] = hi;
-                    // an infinite h has no second part
-                    const float rest = hv - __bfloat162float(hi);
-                    h[a.h_plane] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-                }
-            } else {
-                float acc[2][NT * 8] = {};
-                ffma_rows(a.d, static_cast<const float*>(a.x), a.d, tok, R, acc);
-#pragma unroll
-                for (int r = 0; r < NT * 8; ++r) {
-                    if (r < R) {
-                        const float zg = warp_sum(acc[0][r]), zu = warp_sum(acc[1][r]);
-                        if (lane == (r & 31) && warp < nj)
-                            static_cast<float*>(a.h)[(int64_t)(row0 + r) * a.ldh + j + warp] =
-                                zg / (1.0f + expf(-zg)) * zu;
-                    }
+                for (int kb = 0; kb < a.d; kb += gr.len1) {
+                    const uint32_t bytes = (uint32_t)(min(gr.len1, a.d - kb) * ES);
+                    if (!open(rows, bytes)) return false;
+                    if (src) copy(pos.stage, slot, gr.pitch1, src + (int64_t)kb * ES, bytes);
+                    pos.next(ST);
                 }
             }
-            u += nj;
-        }
-
-        // grid barrier: every CTA's part of h is written
-        __threadfence();
-        consumer_sync();
-        if (tid == 0) {
-            atomicAdd(a.bar, 1u);
-            const unsigned long long t0 = global_timer_ns();
-            for (uint32_t it = 1;; ++it) {
-                unsigned seen;
-                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(a.bar) : "memory");
-                if (seen >= gridDim.x) break;
-                if ((it & 63u) == 0) {
-                    if (*abort_flag) break;
-                    if (global_timer_ns() - t0 > kTimeoutNs) {
-                        *abort_flag = 1;
-                        atomicOr(a.counters + CNT_DEVICE_ERROR, (unsigned long long)DEVERR_TIMEOUT);
-                        break;
+            return true;
+        };
+        // the down stages in order.  Those before `skip` are passed over; of the
+        // next `count`, `weights` opens the stage and copies the weight rows,
+        // `rows` copies the rows of h into it (without weights: into the stages from `at` on)
+        auto down = [&](int skip, int count, bool weights, bool rows, RingPos at) {
+            int n = 0;
+            for (int c = c0; c < c1; c += c_rows) {
+                const int nc = min(c_rows, c1 - c);
+                for (int gi = 0; gi < n_groups; ++gi) {
+                    const FewGroup gr = S.grp[gi];
+                    const int total = nc + PL * gr.R;
+                    const uint8_t* src = nullptr;
+                    int slot = 0;
+                    if (mine < nc) {
+                        src = static_cast<const uint8_t*>(gi < n_act ? a.W_d : a.Ws_d) +
+                              ((int64_t)gr.e * a.d + c + mine) * gr.F * ES;
+                        slot = mine;
+                    } else if (mine < total) {
+                        const int r = mine - nc, pl = r >= gr.R ? 1 : 0;
+                        src = static_cast<const uint8_t*>(a.h) +
+                              ((int64_t)pl * a.h_plane + (int64_t)(gr.row0 + r - pl * gr.R) * a.ldh) * ES;
+                        slot = kFewRows + r;
                     }
-                }
-            }
-        }
-        consumer_sync();
-        __threadfence();
-
-        // down: this CTA's output features, summed over the experts in order
-        for (int c = c0; c < c1; c += kFewRows) {
-            const int nc = min(kFewRows, c1 - c);
-            for (int i = tid; i < (BF16 ? 8 : 1) * NT * 8 * kFewRows; i += 256) yacc[i] = 0.f;
-            consumer_sync();
-            for (int gi = 0; gi < n_groups; ++gi) {
-                const bool routed = gi < n_act;
-                const int e = routed ? S.act[gi] : 0;
-                const int row0 = routed ? S.base[e] : n_rows;
-                const int R = routed ? __popc(S.taken[e]) : a.N;
-                const int K = routed ? a.d_f : a.d_sh;
-                if constexpr (BF16) {
-                    const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(a.h);
-                    const __nv_bfloat16* ptr[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const int r = n * 8 + g;
-                        ptr[n] = r < R ? h + (int64_t)(row0 + r) * a.ldh : nullptr;
-                    }
-                    float acc[NT][4] = {};
-                    mma_rows(K, ptr, 2, a.h_plane, (R + 7) / 8, acc);
-                    // into this warp's sums [token][16 features]: a token has one row in a group
-                    float* mine = yacc + warp * (NT * 8 * kFewRows);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int r = n * 8 + 2 * t + i;
-                            if (r < R) {
-                                const int tk = routed ? S.row_tok[row0 + r] : r;
-                                const float wt = routed ? S.row_w[row0 + r] : 1.f;
-                                mine[tk * kFewRows + g] += wt * acc[n][i];
-                                mine[tk * kFewRows + g + 8] += wt * acc[n][2 + i];
-                            }
+                    const bool go = src && (mine < nc ? weights : rows);
+                    for (int kb = 0; kb < gr.F; kb += gr.len2, ++n) {
+                        if (n < skip) continue;
+                        if (n >= skip + count) return true;
+                        const uint32_t bytes = (uint32_t)(min(gr.len2, gr.F - kb) * ES);
+                        if (weights) {
+                            if (!open(total, bytes)) return false;
+                            at = pos;
+                            pos.next(ST);
                         }
-                    __syncwarp();
-                } else {
-                    float acc[2][NT * 8] = {};
-                    ffma_rows(K, static_cast<const float*>(a.h) + (int64_t)row0 * a.ldh, a.ldh, nullptr, R, acc);
-#pragma unroll
-                    for (int r = 0; r < NT * 8; ++r) {
-                        if (r < R) {
-                            const float s0 = warp_sum(acc[0][r]), s1 = warp_sum(acc[1][r]);
-                            if (lane == 0) {  // features `warp` and `warp + 8` belong to this warp
-                                const int tk = routed ? S.row_tok[row0 + r] : r;
-                                const float wt = routed ? S.row_w[row0 + r] : 1.f;
-                                yacc[tk * kFewRows + warp] += wt * s0;
-                                yacc[tk * kFewRows + warp + 8] += wt * s1;
-                            }
-                        }
+                        if (go) copy(at.stage, slot, gr.pitch2, src + (int64_t)kb * ES, bytes);
+                        if (!weights) at.next(ST);
                     }
                 }
             }
-            consumer_sync();
-            for (int i = tid; i < a.N * kFewRows; i += 256) {
-                const int tk = i / kFewRows, f = i % kFewRows;
-                if (f >= nc) continue;
-                float s = 0.f;
-#pragma unroll
-                for (int q = 0; q < (BF16 ? 8 : 1); ++q) s += yacc[q * (NT * 8 * kFewRows) + i];
-                a.Y[(int64_t)tk * a.d + c + f] = s;
+            return true;
+        };
+        bool ok = gate_up();
+        if (ok) {
+            // a ring full of down weights, then (h is complete) their rows of h, then the rest
+            const RingPos first = pos;
+            ok = down(0, ST, true, false, pos) && warp_wait_bounded(h_ready, 0u, abort_flag, a.counters);
+            if (ok) {
+                // h was written by ordinary stores, of all CTAs; the copies read it
+                asm volatile("fence.proxy.async;" ::: "memory");
+                ok = down(0, ST, false, true, first) && down(ST, 0x7fffffff - ST, true, true, pos);
             }
-            consumer_sync();
         }
-
-        // routing records and statistics, by the first CTA, after its share of the layer
+        // routing records and statistics, by the first CTA's producers, which are done
+        // before the consumers are
         if (blockIdx.x == 0) {
-            for (int i = tid; i < paths; i += 256) {
+            const int ptid = tid - 32 * kFewConsumers;
+            for (int i = ptid; i < paths; i += 32 * kFewProducers) {
                 const int e = S.ids[i], tk = i / a.k;
                 const bool in = e >= 0 && ((S.taken[e] >> tk) & 1u);
                 a.ids[i] = e;
                 a.w[i] = S.w[i];
                 a.slot[i] = in ? __popc(S.taken[e] & ((1u << tk) - 1u)) : -1;
             }
-            for (int i = tid; i < n_rows; i += 256) {
+            for (int i = ptid; i < n_rows; i += 32 * kFewProducers) {
                 a.slot_token[i] = S.row_tok[i];
                 a.slot_w[i] = S.row_w[i];
             }
-            for (int e = tid; e <= a.E; e += 256) {
+            for (int e = ptid; e <= a.E; e += 32 * kFewProducers) {
                 a.offsets[e] = S.base[e];
                 if (e < a.E) {
                     a.L[e] = __popc(S.asked[e]);
@@ -678,8 +595,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                     a.psum[e] = S.psum[e];
                 }
             }
-            if (tid < a.N) a.margin[tid] = S.margin[tid];
-            if (warp == 0) {
+            if (ptid < a.N) a.margin[ptid] = S.margin[ptid];
+            if (ptid < 32) {
                 int req = 0, over = 0, top = 0, affected = 0, skipped = 0;
                 for (int e = lane; e < a.E; e += 32) {
                     const int l = __popc(S.asked[e]);
@@ -720,6 +637,231 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                 }
             }
         }
+        // every copy has landed before the CTA may leave, also when a wait
+        // gave up: the last fill of each used stage, with a limit
+        const unsigned long long t0 = global_timer_ns();
+        for (int s = 0; s < used; ++s) {
+            const uint32_t par = s < pos.stage ? pos.phase : pos.phase ^ 1u;
+            while (!mbar_try_wait(smem_u32(&full[s]), par) && global_timer_ns() - t0 < kTimeoutNs) {
+            }
+        }
+    } else {
+        // ---- consumers ----
+        RingPos pos;
+        const int g = lane >> 2, t = lane & 3;
+        const uint4 zero4 = make_uint4(0, 0, 0, 0);
+        // bf16: one group's 16 weight rows against its R token rows (`planes`
+        // parts each), summed over K: the warps take the steps of 32 in turn
+        auto mma_rows = [&](auto tiles, int K, int piece, int pitch, int R, auto planes,
+                            float (&acc)[4][decltype(tiles)::value][4]) {
+            constexpr int M = decltype(tiles)::value;  // column tiles of 8
+            for (int kb = 0; kb < K; kb += piece) {
+                const int len = min(piece, K - kb);
+                const uint8_t* st = ring + pos.stage * SB;
+                if (warp_wait_bounded(&full[pos.stage], pos.phase, abort_flag, a.counters)) {
+#pragma unroll 4
+                    for (int kk = warp * 32 + t * 8; kk - t * 8 < len; kk += 32 * kFewConsumers) {
+                        const bool in = kk < len;  // what lies behind a row's end in the stage is not a number to use
+                        const uint8_t* col = st + kk * 2;
+                        auto ld = [&](int row, bool have) {
+                            return have && in ? *reinterpret_cast<const uint4*>(col + row * pitch) : zero4;
+                        };
+                        const uint4 lo = ld(g, true), hi = ld(g + 8, true);
+#pragma unroll
+                        for (int n = 0; n < M; ++n) {
+                            if (M == 1 || n * 8 < R) {
+                                const int r = n * 8 + g;
+                                mma_step(acc[0][n], acc[1][n], lo, hi, ld(kFewRows + r, r < R));
+                                if (decltype(planes)::value > 1)
+                                    mma_step(acc[2][n], acc[3][n], lo, hi, ld(kFewRows + R + r, r < R));
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[pos.stage]);
+                pos.next(ST);
+            }
+        };
+        // fp32: weight rows `warp` and `warp + 8` of the stage against R token rows
+        auto ffma_rows = [&](int K, int piece, int pitch, int R, float (&acc)[2][NT * 8]) {
+            for (int kb = 0; kb < K; kb += piece) {
+                const int len = min(piece, K - kb);
+                const uint8_t* st = ring + pos.stage * SB;
+                if (warp_wait_bounded(&full[pos.stage], pos.phase, abort_flag, a.counters)) {
+                    for (int kk = lane * 4; kk < len; kk += 128) {
+                        auto ld = [&](int row) {
+                            return *reinterpret_cast<const float4*>(st + row * pitch + kk * 4);
+                        };
+                        const float4 p = ld(warp), q = ld(warp + 8);
+#pragma unroll
+                        for (int r = 0; r < NT * 8; ++r) {
+                            if (r < R) {
+                                const float4 v = ld(kFewRows + r);
+                                acc[0][r] += p.x * v.x + p.y * v.y + p.z * v.z + p.w * v.w;
+                                acc[1][r] += q.x * v.x + q.y * v.y + q.z * v.z + q.w * v.w;
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[pos.stage]);
+                pos.next(ST);
+            }
+        };
+
+        // the form for a group's rows: as many column tiles as they fill (a
+        // group of a few rows in a batch of 32 tokens needs one, not four)
+        auto by_rows = [&](int R, auto f) {
+            if (NT > 1 && R <= 8) f(std::integral_constant<int, 1>{});
+            else if (NT > 2 && R <= 16) f(std::integral_constant<int, 2>{});
+            else f(std::integral_constant<int, NT>{});
+        };
+        const std::integral_constant<int, 1> x_parts{};
+        const std::integral_constant<int, 2> h_parts{};
+
+        // gate/up: h of this CTA's hidden units
+        int tile = 0, nj;
+        for (int gi = S.from[0], j = S.from[1]; unit_tile(gi, j, nj); j += nj, ++tile) {
+            const FewGroup gr = S.grp[gi];
+            const int row0 = gr.row0, R = gr.R;
+            if constexpr (BF16) {
+                // warps' partial sums: [n][16 rows][8 columns], two buffers in turn
+                float* mine = red + ((tile & 1) * 8 + warp) * (NT * 128);
+                by_rows(R, [&](auto tiles) {
+                    constexpr int M = decltype(tiles)::value;
+                    float part[4][M][4] = {};
+                    mma_rows(tiles, a.d, gr.len1, gr.pitch1, R, x_parts, part);
+#pragma unroll
+                    for (int n = 0; n < M; ++n) {
+                        float c[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) c[i] = part[0][n][i] + part[1][n][i];
+                        *reinterpret_cast<float2*>(mine + n * 128 + g * 8 + 2 * t) = make_float2(c[0], c[1]);
+                        *reinterpret_cast<float2*>(mine + n * 128 + (g + 8) * 8 + 2 * t) = make_float2(c[2], c[3]);
+                    }
+                });
+                consumer_sync();
+                const int unit = tid & 7, r = tid >> 3;
+                if (r < R && unit < nj) {
+                    const float* p = red + (tile & 1) * 8 * (NT * 128) + (r >> 3) * 128 + unit * 8 + (r & 7);
+                    float zg = 0.f, zu = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        zg += p[q * (NT * 128)];
+                        zu += p[q * (NT * 128) + 64];
+                    }
+                    const float hv = zg / (1.0f + expf(-zg)) * zu;
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(hv);
+                    __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.h) + (int64_t)(row0 + r) * a.ldh + j + unit;
+                    h[0] = hi;
+                    // an infinite h has no second part
+                    const float rest = hv - __bfloat162float(hi);
+                    h[a.h_plane] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+                }
+            } else {
+                float acc[2][NT * 8] = {};
+                ffma_rows(a.d, gr.len1, gr.pitch1, R, acc);
+#pragma unroll
+                for (int r = 0; r < NT * 8; ++r) {
+                    if (r < R) {
+                        const float zg = warp_sum(acc[0][r]), zu = warp_sum(acc[1][r]);
+                        if (lane == (r & 31) && warp < nj)
+                            static_cast<float*>(a.h)[(int64_t)(row0 + r) * a.ldh + j + warp] =
+                                zg / (1.0f + expf(-zg)) * zu;
+                    }
+                }
+            }
+        }
+
+        // grid barrier: every CTA's part of h is written, also for the copies that will read it
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __threadfence();
+        consumer_sync();
+        if (tid == 0) {
+            atomicAdd(a.bar, 1u);
+            const unsigned long long t0 = global_timer_ns();
+            for (uint32_t it = 1;; ++it) {
+                unsigned seen;
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(a.bar) : "memory");
+                if (seen >= gridDim.x) break;
+                if ((it & 63u) == 0) {
+                    if (*abort_flag) break;
+                    if (global_timer_ns() - t0 > kTimeoutNs) {
+                        *abort_flag = 1;
+                        atomicOr(a.counters + CNT_DEVICE_ERROR, (unsigned long long)DEVERR_TIMEOUT);
+                        break;
+                    }
+                }
+            }
+        }
+        consumer_sync();
+        __threadfence();
+        if (tid == 0) mbar_arrive(h_ready);
+
+        // down: this CTA's output features, summed over the experts in order
+        for (int c = c0; c < c1; c += c_rows) {
+            const int nc = min(c_rows, c1 - c);
+            for (int i = tid; i < (BF16 ? 8 : 1) * NT * 8 * kFewRows; i += 256) yacc[i] = 0.f;
+            consumer_sync();
+            for (int gi = 0; gi < n_groups; ++gi) {
+                const bool routed = gi < n_act;
+                const FewGroup gr = S.grp[gi];
+                const int row0 = gr.row0, R = gr.R;
+                if constexpr (BF16) {
+                    // into this warp's sums [token][16 features]: a token has one row in a group
+                    float* mine = yacc + warp * (NT * 8 * kFewRows);
+                    by_rows(R, [&](auto tiles) {
+                        constexpr int M = decltype(tiles)::value;
+                        float part[4][M][4] = {};
+                        mma_rows(tiles, gr.F, gr.len2, gr.pitch2, R, h_parts, part);
+#pragma unroll
+                        for (int n = 0; n < M; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int r = n * 8 + 2 * t + i;
+                                if (r < R) {
+                                    const int tk = routed ? S.row_tok[row0 + r] : r;
+                                    const float wt = routed ? S.row_w[row0 + r] : 1.f;
+                                    const float lo =
+                                        (part[0][n][i] + part[1][n][i]) + (part[2][n][i] + part[3][n][i]);
+                                    const float hi = (part[0][n][2 + i] + part[1][n][2 + i]) +
+                                                     (part[2][n][2 + i] + part[3][n][2 + i]);
+                                    mine[tk * kFewRows + g] += wt * lo;
+                                    mine[tk * kFewRows + g + 8] += wt * hi;
+                                }
+                            }
+                    });
+                    __syncwarp();
+                } else {
+                    float acc[2][NT * 8] = {};
+                    ffma_rows(gr.F, gr.len2, gr.pitch2, R, acc);
+#pragma unroll
+                    for (int r = 0; r < NT * 8; ++r) {
+                        if (r < R) {
+                            const float s0 = warp_sum(acc[0][r]), s1 = warp_sum(acc[1][r]);
+                            if (lane == 0) {  // features `warp` and `warp + 8` belong to this warp
+                                const int tk = routed ? S.row_tok[row0 + r] : r;
+                                const float wt = routed ? S.row_w[row0 + r] : 1.f;
+                                yacc[tk * kFewRows + warp] += wt * s0;
+                                yacc[tk * kFewRows + warp + 8] += wt * s1;
+                            }
+                        }
+                    }
+                }
+            }
+            consumer_sync();
+            for (int i = tid; i < a.N * kFewRows; i += 256) {
+                const int tk = i / kFewRows, f = i % kFewRows;
+                if (f >= nc) continue;
+                float s = 0.f;
+#pragma unroll
+                for (int q = 0; q < (BF16 ? 8 : 1); ++q) s += yacc[q * (NT * 8 * kFewRows) + i];
+                a.Y[(int64_t)tk * a.d + c + f] = s;
+            }
+            consumer_sync();
+        }
+
     }
     __syncthreads();
 }
@@ -736,19 +878,22 @@ cudaError_t launch_layer(const FewArgs& a, cudaStream_t st) {
     auto kern = few_layer_kernel<BF16, NT>;
     const size_t smem = few_smem(BF16, NT);
     static_assert(few_smem(BF16, NT) <= 232448, "shared memory per CTA");
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem_once<few_layer_kernel<BF16, NT>>(smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)num_sms(), 1, 1);
     cfg.blockDim = dim3(kFewThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    // all CTAs are resident together: they meet at a grid barrier
-    cudaLaunchAttribute attr[1];
+    // all CTAs are resident together: they meet at a grid barrier.  They are
+    // set up while the scores kernel runs
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, kern, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

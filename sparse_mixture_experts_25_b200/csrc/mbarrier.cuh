@@ -61,24 +61,24 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
     }
 }
 
-// Warp-collective bounded wait: every lane returns the same result, so the
-// .sync.aligned tcgen05 loads that follow are executed by the whole warp.
-__device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity,
-                                                  volatile int* abort_flag,
+// Warp-collective bounded wait: every lane returns the same result.  The timer
+// is read only once a wait has gone on for a while: reading %globaltimer costs
+// far more than a wait that is already over.
+__device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                   unsigned long long* counters) {
     const uint32_t a = smem_u32(bar);
     const int lane = threadIdx.x & 31;
     unsigned long long t0 = 0;
-    if (lane == 0) t0 = global_timer_ns();
     for (uint32_t it = 0;; ++it) {
-        const bool done = mbar_try_wait(a, parity);
-        if (__all_sync(0xffffffffu, done)) return true;
+        if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
         if ((it & 63u) == 63u) {
             int stop = 0;
             if (lane == 0) {
+                const unsigned long long now = global_timer_ns();
+                if (t0 == 0) t0 = now;
                 if (*abort_flag) {
                     stop = 1;
-                } else if (global_timer_ns() - t0 > kTimeoutNs) {
+                } else if (now - t0 > kTimeoutNs) {
                     *abort_flag = 1;
                     atomicOr(counters + CNT_DEVICE_ERROR, (unsigned long long)DEVERR_TIMEOUT);
                     stop = 1;

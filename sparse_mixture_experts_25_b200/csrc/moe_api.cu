@@ -299,8 +299,9 @@ static moe_status check_few(const moe_params* p) {
         record_error("moe_forward_few: rerouting and acceptance by weight are moe_forward's");
         return MOE_ERR_UNSUPPORTED;
     }
-    if ((int64_t)p->E_r * p->d_f + p->d_f_shared >= (int64_t)1 << 31) {
-        record_error("moe_forward_few: E_r d_f + d_f_shared must be below 2^31");
+    // costs of the hidden units are summed in 32 bits, at most 255 each
+    if ((int64_t)p->E_r * p->d_f + p->d_f_shared >= (int64_t)1 << 24 || p->d >= 1 << 24) {
+        record_error("moe_forward_few: E_r d_f + d_f_shared and d must be below 2^24");
         return MOE_ERR_UNSUPPORTED;
     }
     return MOE_OK;

@@ -230,6 +230,20 @@ cudaError_t launch_few(const moe_params& p, int64_t C, const void* x, const void
 
 int num_sms();
 
+// Lets `kern` use `smem` bytes of dynamic shared memory on the current device;
+// asked of the driver once per device (a repeated request would be harmless)
+template <auto kern>
+inline cudaError_t allow_smem_once(size_t smem) {
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
 // ---------------------------------------------------------------------------
 // Device helpers
 // ---------------------------------------------------------------------------

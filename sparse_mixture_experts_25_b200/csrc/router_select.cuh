@@ -66,32 +66,39 @@ __device__ __forceinline__ void select_token(const RouterArgs& a, int64_t t, int
     const int want = k + (a.X > 1 ? a.X : 1);
     const int rounds = want < E ? want : E;
     if (!__any_sync(0xffffffffu, bad)) {
-        for (int r = 0; r < rounds; ++r) {
-            float bv = -INFINITY;
-            int be = 0x7fffffff;
+        // order-preserving integer keys (-0 counts as 0), so that the warp's
+        // maximum and the lowest index that has it are one instruction each
+        auto best = [&](uint32_t& bk, int& be) {
+            bk = 0u;
+            be = 0x7fffffff;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int e = lane + 32 * i;
-                if (!((taken >> i) & 1u) && e < E && (v[i] > bv || (v[i] == bv && e < be))) {
-                    bv = v[i];
+                const uint32_t u = __float_as_uint(v[i] + 0.f);
+                const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+                if (!((taken >> i) & 1u) && e < E && key > bk) {
+                    bk = key;
                     be = e;
                 }
             }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-                const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-                if (ov > bv || (ov == bv && oe < be)) {
-                    bv = ov;
-                    be = oe;
-                }
-            }
+        };
+        uint32_t bk;
+        int be;
+        best(bk, be);
+        for (int r = 0; r < rounds; ++r) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
+            const int te = (int)__reduce_min_sync(0xffffffffu, bk == top ? (unsigned)be : 0x7fffffffu);
+            const uint32_t u = top & 0x80000000u ? top ^ 0x80000000u : ~top;
+            const float tv = __uint_as_float(u);
             if (lane == r) {
-                my_e = be;
-                my_g = bv;
+                my_e = te;
+                my_g = tv;
             }
-            if (r == k) next_g = bv;
-            if ((be & 31) == lane) taken |= 1u << (be >> 5);
+            if (r == k) next_g = tv;
+            if ((te & 31) == lane) {
+                taken |= 1u << (te >> 5);
+                best(bk, be);
+            }
         }
     }
     float z = 0.f;
