@@ -629,6 +629,72 @@ MOE_API moe_status moe_backward(const moe_params* p, float aux_coef, const int32
 MOE_API moe_status moe_backward_check(const moe_params* p, const void* bws, moe_stream_t stream);
 
 /*
+ * Low-rank adapters of many requests at once, beside a shared projection or
+ * beside the layer.  Token t carries the adapter ids[t] = a, or none (-1);
+ * with u_t = scale_a A_a x_t,
+ *   y_t = base_t + W x_t + B_a u_t,
+ * the adapter's term absent for ids[t] = -1.  W null: no projection (beside
+ * the layer: base = y = the layer's output, to which the terms are added).
+ *   x    [N, d_in] dtype          W     [d_out, d_in] dtype, nullable
+ *   A    [n_adapters, r, d_in] dtype   B  [n_adapters, d_out, r] dtype
+ *   scale [n_adapters] fp32       ids   [N] int32
+ *   base [N, d_out] fp32, nullable (0); may be y itself, except with W
+ *        (MOE_ERR_INVALID_ARG).  Other overlaps are not allowed.
+ *   y    [N, d_out] fp32, overwritten
+ * Tokens of one adapter may stand anywhere in the batch.
+ *
+ * moe_adapter_backward: the gradients for dy = dL/dy, with v_t = scale_a
+ * B_a^T dy_t,
+ *   dx_t = dx_base_t + W^T dy_t + A_a^T v_t
+ *   dA_a = sum_t v_t x_t^T,   dB_a = sum_t dy_t u_t^T   (a's tokens)
+ * W, scale and base have no gradient here (base's is dy itself; W is frozen).
+ *   dy [N, d_out] fp32; dx_base [N, d_in] fp32, nullable, may be dx except
+ *   with W; dx [N, d_in], dA [n_adapters, r, d_in], dB [n_adapters, d_out, r]
+ *   fp32, overwritten (adapters without tokens get zeros).
+ * It needs nothing of the forward call.
+ *
+ * Precision: fp32 accumulation.  16-bit operands are used as they are; fp32
+ * operands of bf16 calls (u, v, dy) as two bf16 parts (16 mantissa bits), of
+ * fp32 calls as three (24 bits), except the fp32 projection, which runs on the
+ * CUDA cores.  Same inputs give the same bits without W; with W the projection
+ * may split K over CTAs (fp32 additions in any order).
+ * Constraints: d_in, d_out and r multiples of 8, r <= 128, n_adapters <= 1024,
+ * N < 2^30 (fp32 with W: N <= 65535 * 64); else MOE_ERR_UNSUPPORTED.  Pointers
+ * of x, W, A, B, base, y, dy, dx, dA, dB and ws 16-byte aligned.
+ * An id outside -1 .. n_adapters - 1 counts as -1 and is reported by
+ * moe_adapter_check.  N = 0 writes nothing (backward: zeroes dA and dB).
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
+ * MOE_ERR_CUDA.  Asynchronous on `stream`, no allocation; may be captured
+ * into a CUDA graph (make the first call on a device outside a capture).
+ */
+typedef struct moe_adapter_params {
+    int64_t N;           /* tokens                                             */
+    int32_t d_in;        /* width of x                                         */
+    int32_t d_out;       /* width of y                                         */
+    int32_t n_adapters;  /* adapters held in A, B and scale                    */
+    int32_t r;           /* rank (adapters of a smaller rank are zero-padded)  */
+    int32_t dtype;       /* moe_dtype of x, W, A and B                         */
+    int32_t reserved;    /* 0                                                  */
+} moe_adapter_params;
+
+/* Workspace bytes (host); with_W: whether the calls give a projection. */
+MOE_API moe_status moe_adapter_workspace_size(const moe_adapter_params* p, int with_W, size_t* bytes);
+MOE_API moe_status moe_adapter_backward_workspace_size(const moe_adapter_params* p, int with_W, size_t* bytes);
+
+MOE_API moe_status moe_adapter_forward(const moe_adapter_params* p, const void* x, const void* W, const void* A,
+                                       const void* B, const float* scale, const int32_t* ids, const float* base,
+                                       float* y, void* ws, moe_stream_t stream);
+MOE_API moe_status moe_adapter_backward(const moe_adapter_params* p, const void* x, const void* W, const void* A,
+                                        const void* B, const float* scale, const int32_t* ids, const float* dy,
+                                        const float* dx_base, float* dx, float* dA, float* dB, void* ws,
+                                        moe_stream_t stream);
+
+/* Waits for `stream`; MOE_ERR_INVALID_ARG if the last adapter call on `ws` met
+ * an id out of range, MOE_ERR_TIMEOUT if a bounded device wait of its
+ * projection gave up, else MOE_OK. */
+MOE_API moe_status moe_adapter_check(const moe_adapter_params* p, const void* ws, moe_stream_t stream);
+
+/*
  * Self-test of the library's bounded device waits (no counterpart on the
  * pages).  Launches one CTA that waits on a shared-memory mbarrier nothing
  * ever arrives on, with the same bounded-wait routine the tensor-core GEMMs

@@ -27,6 +27,8 @@ __all__ = [
     "moe_dispatch_ranked", "moe_gather_rows", "workspace_x_perm",
     "moe_ep_plan", "moe_ep_dispatch", "moe_ep_combine", "pointer_table",
     "moe_soft_check",
+    "AdapterParams", "adapter_params", "moe_adapter_workspace_size", "moe_adapter_backward_workspace_size",
+    "moe_adapter_forward", "moe_adapter_backward", "moe_adapter_check",
     "workspace_views", "HEADER",
 ]
 
@@ -67,6 +69,18 @@ class SoftParams(ctypes.Structure):
 def soft_params(N, d, d_f, E_r, p, dtype=None) -> SoftParams:
     """Soft MoE layer: S = E_r p slots (see moe_soft_forward in the header)."""
     return SoftParams(int(N), int(d), int(d_f), int(E_r), int(p), int(MOE_BF16 if dtype is None else dtype), 0)
+
+
+class AdapterParams(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32),
+                ("n_adapters", ctypes.c_int32), ("r", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+def adapter_params(N, d_in, d_out, n_adapters, r, dtype=None) -> AdapterParams:
+    """Low-rank adapters of many requests (see moe_adapter_forward in the header)."""
+    return AdapterParams(int(N), int(d_in), int(d_out), int(n_adapters), int(r),
+                         int(MOE_BF16 if dtype is None else dtype), 0)
 
 
 class Stats(ctypes.Structure):
@@ -141,6 +155,12 @@ def lib():
         L.moe_backward.argtypes = [pp, ctypes.c_float, ctypes.POINTER(ctypes.c_int32), _P, _P, _P, _P, _P, _P,
                                    _P, _P, _P, _P, _P, ctypes.POINTER(Grads), _P, ctypes.c_size_t, _P]
         L.moe_backward_check.argtypes = [pp, _P, _P]
+        ap = ctypes.POINTER(AdapterParams)
+        L.moe_adapter_workspace_size.argtypes = [ap, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_adapter_backward_workspace_size.argtypes = [ap, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_adapter_forward.argtypes = [ap] + [_P] * 10
+        L.moe_adapter_backward.argtypes = [ap] + [_P] * 13
+        L.moe_adapter_check.argtypes = [ap, _P, _P]
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         L.moe_status_string.argtypes = [ctypes.c_int]
@@ -152,7 +172,9 @@ def lib():
                      "moe_forward_end", "moe_selftest_wait_timeout", "moe_soft_workspace_size",
                      "moe_soft_forward", "moe_soft_check", "moe_dispatch_ranked", "moe_gather_rows",
                      "moe_backward_workspace_size", "moe_backward", "moe_backward_check",
-                     "moe_few_workspace_size", "moe_forward_few"):
+                     "moe_few_workspace_size", "moe_forward_few", "moe_adapter_workspace_size",
+                     "moe_adapter_backward_workspace_size", "moe_adapter_forward", "moe_adapter_backward",
+                     "moe_adapter_check"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -213,15 +235,22 @@ class _on_device_of:
     launches on the current device and, without a stream, on its current
     stream); tensors of several devices are refused."""
 
+    __slots__ = ("index", "guard")
+
     def __init__(self, *tensors):
-        index = {t.device.index for t in tensors if hasattr(t, "is_cuda") and t.is_cuda}
-        if len(index) > 1:
-            raise ValueError("libmoe takes tensors of one device; got devices %s" % sorted(index))
-        self.index = index.pop() if index else None
-        self.guard = None
+        self.index, self.guard = -1, None
+        for t in tensors:
+            if t is not None and not isinstance(t, int):
+                i = t.get_device()
+                if i != self.index:
+                    if i < 0:
+                        raise ValueError("libmoe takes device tensors; got a host tensor")
+                    if self.index >= 0:
+                        raise ValueError("libmoe takes tensors of one device; got devices %d and %d" % (self.index, i))
+                    self.index = i
 
     def __enter__(self):
-        if self.index is not None:
+        if self.index >= 0:
             import torch
             if torch.cuda.current_device() != self.index:
                 self.guard = torch.cuda.device(self.index)
@@ -501,3 +530,73 @@ def moe_backward_check(p, bws, stream=None) -> int:
     moe_backward on bws gave up, MOE_ERR_INVALID_ARG if its offsets_host
     differed from the forward's device offsets, else MOE_OK."""
     return lib().moe_backward_check(ctypes.byref(p), _ptr(bws), _stream(stream))
+
+
+def moe_adapter_workspace_size(ap: AdapterParams, with_W: bool = False) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_adapter_workspace_size(ctypes.byref(ap), int(bool(with_W)), ctypes.byref(n)),
+           "moe_adapter_workspace_size")
+    return n.value
+
+
+def moe_adapter_backward_workspace_size(ap: AdapterParams, with_W: bool = False) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_adapter_backward_workspace_size(ctypes.byref(ap), int(bool(with_W)), ctypes.byref(n)),
+           "moe_adapter_backward_workspace_size")
+    return n.value
+
+
+def _typed(what, t, dtype, shape):
+    """Refuses a tensor of another type or shape than the call's."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _adapter_types(ap, x, W, A, B, scale, ids):
+    import torch
+    dt = torch.bfloat16 if ap.dtype == MOE_BF16 else torch.float32
+    _typed("x", x, dt, (ap.N, ap.d_in))
+    if W is not None:
+        _typed("W", W, dt, (ap.d_out, ap.d_in))
+    _typed("A", A, dt, (ap.n_adapters, ap.r, ap.d_in))
+    _typed("B", B, dt, (ap.n_adapters, ap.d_out, ap.r))
+    _typed("scale", scale, torch.float32, (ap.n_adapters,))
+    _typed("ids", ids, torch.int32, (ap.N,))
+    return torch.float32
+
+
+def moe_adapter_forward(ap, x, W, A, B, scale, ids, base, y, ws, stream=None):
+    """y = base + x W^T + the low-rank term of each token's adapter (see
+    moe_adapter_forward in include/moe.h); W and base may be None, and base
+    may be y itself without W."""
+    f32 = _adapter_types(ap, x, W, A, B, scale, ids)
+    for what, t in (("base", base), ("y", y)):
+        if t is not None:
+            _typed(what, t, f32, (ap.N, ap.d_out))
+    with _on_device_of(x, W, A, B, scale, ids, base, y, ws):
+        _check(lib().moe_adapter_forward(ctypes.byref(ap), _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(scale), _ptr(ids),
+                                         _ptr(base), _ptr(y), _ptr(ws), _stream(stream)), "moe_adapter_forward")
+
+
+def moe_adapter_backward(ap, x, W, A, B, scale, ids, dy, dx_base, dx, dA, dB, ws, stream=None):
+    """dx, dA and dB for the upstream gradient dy (see moe_adapter_backward in
+    include/moe.h); W and dx_base may be None, and dx_base may be dx itself
+    without W."""
+    f32 = _adapter_types(ap, x, W, A, B, scale, ids)
+    _typed("dy", dy, f32, (ap.N, ap.d_out))
+    for what, t in (("dx_base", dx_base), ("dx", dx)):
+        if t is not None:
+            _typed(what, t, f32, (ap.N, ap.d_in))
+    _typed("dA", dA, f32, (ap.n_adapters, ap.r, ap.d_in))
+    _typed("dB", dB, f32, (ap.n_adapters, ap.d_out, ap.r))
+    with _on_device_of(x, W, A, B, scale, ids, dy, dx_base, dx, dA, dB, ws):
+        _check(lib().moe_adapter_backward(ctypes.byref(ap), _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(scale),
+                                          _ptr(ids), _ptr(dy), _ptr(dx_base), _ptr(dx), _ptr(dA), _ptr(dB),
+                                          _ptr(ws), _stream(stream)), "moe_adapter_backward")
+
+
+def moe_adapter_check(ap, ws, stream=None) -> int:
+    """Waits for the stream; MOE_ERR_INVALID_ARG if the last adapter call on ws
+    met an id out of range, MOE_ERR_TIMEOUT, or MOE_OK."""
+    with _on_device_of(ws):
+        return lib().moe_adapter_check(ctypes.byref(ap), _ptr(ws), _stream(stream))

@@ -1,0 +1,1185 @@
+// Low-rank adapters of many requests at once, beside a shared projection or
+// beside the whole layer, with their gradients.
+//
+// Token t has adapter a = ids[t] (or none).  With u_t = s_a A_a x_t and
+// v_t = s_a B_a^T dy_t (both r numbers):
+//   forward    y_t  = base_t + W x_t + B_a u_t
+//   backward   dx_t = base_t + W^T dy_t + A_a^T v_t
+//              dA_a = sum_t v_t x_t^T,  dB_a = sum_t dy_t u_t^T
+// over the tokens of adapter a.
+//
+// What bounds them: r is 8 to 128 while the widths are thousands, so each step
+// reads one [N, width] array and writes another or none; the floor is those
+// bytes.  Three kinds of kernel, each one pass over its wide array:
+//   shrink  [N, K] x [K, r]  -> u or v        reads x or dy
+//   expand  [N, r] x [r, J]  -> y or dx       reads base, writes y or dx
+//   grad    [r, n] x [n, J]  -> dA or dB      reads x or dy over a's tokens
+// A stable counting sort (plan) puts the tokens of an adapter next to one
+// another, so a tile of 64 rows has one adapter and reads it once; the rows are
+// gathered and scattered where they are used, not copied.  The sort is stable
+// and nothing is summed by atomics: results do not depend on the schedule.
+//
+// Arithmetic: mma.sync m16n8k16 on bf16 parts, fp32 accumulation.  A 16-bit
+// operand is one part; a 32-bit one is the sum of bf16 parts, two (16 bits)
+// beside 16-bit adapters and three (24 bits) in fp32, where the products of
+// parts up to 2^-16 of the first are kept.  (tcgen05 tiles of 64 or 128 rows
+// would be mostly padding at these ranks: the tensor pipe is not what bounds.)
+// u and v are stored as such parts, in the sorted order.
+//
+// A few tokens (N <= 32) take another form: no sort, one CTA per token and
+// slice of K, then one thread per output; two launches instead of three, and no
+// row of a tile is wasted on a token with an adapter of its own.
+//
+// W runs on the layer's own GEMMs (tcgen05 for bf16, dy as two bf16 parts).
+#include "moe_internal.cuh"
+
+#include <cooperative_groups.h>
+#include <stdio.h>
+
+#include <algorithm>
+#include <type_traits>
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+namespace {
+
+constexpr int kRows = 64;          // rows of a tile
+constexpr int kShrinkK = 64;       // K elements staged at a time
+constexpr int kExpandCols = 128;   // columns staged at a time
+constexpr int kGradCols = 128;     // columns of a grad CTA
+constexpr int kGradRows = 32;      // tokens staged at a time
+constexpr int kFewN = 32;          // batches of the few-token form
+constexpr int kMaxSlices = 8;      // K slices of a shrink (CTAs of a cluster)
+constexpr int kMaxSplits = 8;      // token splits of a grad
+
+// bf16 parts of an operand: of type T itself, and of an fp32 one beside T
+template <typename T>
+struct Parts;
+template <>
+struct Parts<__nv_bfloat16> {
+    static constexpr int self = 1, f32 = 2;
+};
+template <>
+struct Parts<float> {
+    static constexpr int self = 3, f32 = 3;
+};
+template <typename TA, typename T>
+constexpr int act_parts() {
+    return std::is_same<TA, T>::value ? Parts<T>::self : Parts<T>::f32;
+}
+
+struct Tile {
+    int32_t adapter, pos, rows, pad;  // adapter n_adapters: the tokens that have none
+};
+
+struct Plan {
+    int32_t* perm;      // [N] token at each sorted position
+    int32_t* seg;       // [n_adapters + 2] first position of each adapter; tokens without one last
+    Tile* tiles;        // tiles of at most kRows rows, one adapter each
+    int32_t* n_tiles;
+    int32_t* one_group; // {0, N} and {0, ceil(N / 128)}: the dense W^T dy as a group of rows
+    unsigned long long* counters;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void* p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"((uint32_t)__cvta_generic_to_shared(p)));
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// v = sum of P bf16 parts, each the rounding of what the ones before leave.
+// A value that is not finite is its first part; the others are 0.
+template <int P>
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&out)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        out[i] = pack2(a, b);
+        if (i + 1 < P) {
+            const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&out[i]);
+            a -= __bfloat162float(v.x);
+            b -= __bfloat162float(v.y);
+            if (!isfinite(a)) a = 0.f;
+            if (!isfinite(b)) b = 0.f;
+        }
+    }
+}
+
+// eight consecutive elements as P parts of four packed pairs
+template <int P>
+__device__ __forceinline__ void load8_parts(const __nv_bfloat16* p, bool in, uint4 (&out)[P]) {
+    static_assert(P == 1, "16-bit operands are one part");
+    out[0] = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+}
+template <int P>
+__device__ __forceinline__ void load8_parts(const float* p, bool in, uint4 (&out)[P]) {
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 lo = in ? *reinterpret_cast<const float4*>(p) : zero;
+    const float4 hi = in ? *reinterpret_cast<const float4*>(p + 4) : zero;
+    uint32_t a[P], b[P], c[P], d[P];
+    split2<P>(lo.x, lo.y, a);
+    split2<P>(lo.z, lo.w, b);
+    split2<P>(hi.x, hi.y, c);
+    split2<P>(hi.z, hi.w, d);
+#pragma unroll
+    for (int i = 0; i < P; ++i) out[i] = make_uint4(a[i], b[i], c[i], d[i]);
+}
+
+// whether the product of parts i and j counts beside operands of PA and PB parts
+template <int PA, int PB>
+__device__ __forceinline__ constexpr bool counts(int i, int j) {
+    return i + j < (PA > PB ? PA : PB);
+}
+
+// ---------------------------------------------------------------------------
+// Plan: a stable counting sort of the tokens by adapter, by one CTA.  Warp w
+// walks tokens [w chunk, (w+1) chunk) in order; lanes with the same adapter
+// take consecutive places.  Ids out of range count as none and are reported.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t* ids, int N, int n_adapters, Plan p) {
+    extern __shared__ int32_t sm[];
+    const int nb = n_adapters + 1;
+    int32_t* cnt = sm;               // [32][nb] tokens of bucket b before warp w's next one
+    int32_t* first = sm + 32 * nb;   // [nb + 1]
+    int32_t* tile0 = first + nb + 1; // [nb + 1]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < 32 * nb; i += 1024) cnt[i] = 0;
+    if (tid < CNT_COUNT) p.counters[tid] = 0ull;
+    __syncthreads();
+    const int chunk = ((N + 31) / 32 + 31) / 32 * 32;
+    const int t0 = warp * chunk, t1 = min(N, t0 + chunk);
+    bool bad = false;
+    auto bucket = [&](int t) {
+        if (t >= t1) return -1;
+        const int id = ids[t];
+        if (id < -1 || id >= n_adapters) bad = true;
+        return id < 0 || id >= n_adapters ? n_adapters : id;
+    };
+    for (int b = t0; b < t1; b += 32) {
+        const int id = bucket(b + lane);
+        const unsigned same = __match_any_sync(0xffffffffu, id);
+        if (id >= 0 && lane == __ffs(same) - 1) cnt[warp * nb + id] += __popc(same);
+        __syncwarp();
+    }
+    if (bad) atomicOr(p.counters + CNT_DEVICE_ERROR, (unsigned long long)DEVERR_BOUNDS);
+    __syncthreads();
+    for (int b = tid; b < nb; b += 1024) {  // exclusive over the warps, total in first[b]
+        int s = 0;
+        for (int w = 0; w < 32; ++w) {
+            const int c = cnt[w * nb + b];
+            cnt[w * nb + b] = s;
+            s += c;
+        }
+        first[b] = s;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int rows = 0, tiles = 0;
+        for (int b = 0; b < nb; b += 32) {
+            const int c = b + lane < nb ? first[b + lane] : 0, t = (c + kRows - 1) / kRows;
+            int sc = c, st = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, sc, o), v = __shfl_up_sync(0xffffffffu, st, o);
+                if (lane >= o) {
+                    sc += u;
+                    st += v;
+                }
+            }
+            __syncwarp();
+            if (b + lane < nb) {
+                first[b + lane] = rows + sc - c;
+                tile0[b + lane] = tiles + st - t;
+            }
+            rows += __shfl_sync(0xffffffffu, sc, 31);
+            tiles += __shfl_sync(0xffffffffu, st, 31);
+        }
+        if (lane == 0) {
+            first[nb] = rows;
+            tile0[nb] = tiles;
+            *p.n_tiles = tiles;
+            p.one_group[0] = 0;
+            p.one_group[1] = N;
+            p.one_group[2] = 0;
+            p.one_group[3] = (N + 127) / 128;
+        }
+    }
+    __syncthreads();
+    for (int b = tid; b <= nb; b += 1024) p.seg[b] = first[b];
+    for (int i = tid; i < tile0[nb]; i += 1024) {
+        int lo = 0, hi = nb - 1;  // the last bucket whose tiles begin at or before i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tile0[mid] <= i) lo = mid;
+            else hi = mid - 1;
+        }
+        const int pos = first[lo] + (i - tile0[lo]) * kRows;
+        p.tiles[i] = {lo, pos, min(kRows, first[lo + 1] - pos), 0};
+    }
+    for (int b = t0; b < t1; b += 32) {
+        const int t = b + lane, id = bucket(t);
+        const unsigned same = __match_any_sync(0xffffffffu, id);
+        int at = 0;
+        if (id >= 0) at = first[id] + cnt[warp * nb + id] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (id >= 0) {
+            if (lane == __ffs(same) - 1) cnt[warp * nb + id] += __popc(same);
+            p.perm[at] = t;
+        }
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// shrink: out[pos, q] = s_a sum_k X[tok(pos), k] M_a(q, k) as parts.
+//   NN = false: M_a is A_a [r, K] (x -> u);  NN = true: M_a is B_a [K, r] (dy -> v)
+// A CTA has one tile and one of the cluster's K slices; each warp 16 of the
+// rows.  X goes from global memory to the MMA's A registers: a lane reads 8
+// consecutive K elements of two rows and feeds them to two MMAs, the adapter's
+// elements in the same order of K.  The cluster's CTAs add their sums in slice
+// order through distributed shared memory.
+// ---------------------------------------------------------------------------
+struct ShrinkArgs {
+    const void* X;
+    const void* M;
+    const float* scale;
+    int K, r, n_adapters, slice;
+    int64_t N;
+    __nv_bfloat16* out;  // [parts][N][r]
+    Plan p;
+};
+
+template <typename T, typename TA, bool NN, int NQ>
+__global__ void __launch_bounds__(128) adapter_shrink_kernel(const __grid_constant__ ShrinkArgs a) {
+    constexpr int PA = act_parts<TA, T>(), PB = Parts<T>::self, PF = Parts<T>::f32;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const cg::cluster_group cluster = cg::this_cluster();
+    if ((int)blockIdx.x >= *a.p.n_tiles) return;  // the same for the whole cluster
+    const Tile tile = a.p.tiles[blockIdx.x];
+    if (tile.adapter >= a.n_adapters) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int r = a.r;
+    // NN: [64 k][r] rows in the order that ldmatrix wants; else [r][64 k]
+    const int pitch = NN ? r * 2 + 16 : kShrinkK * 2 + 64;
+    const int part_bytes = (NN ? kShrinkK : r) * pitch;
+    const TA* X = static_cast<const TA*>(a.X);
+    const T* M = static_cast<const T*>(a.M) + (int64_t)tile.adapter * r * a.K;
+    const TA* row[2];
+    bool have[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int q = warp * 16 + g + 8 * i;
+        have[i] = q < tile.rows;
+        row[i] = X + (int64_t)(have[i] ? a.p.perm[tile.pos + q] : 0) * a.K;
+    }
+    float acc[NQ][4] = {};
+    const int k_end = min(a.K, (int)(blockIdx.y + 1) * a.slice);
+    for (int kb = blockIdx.y * a.slice; kb < k_end; kb += kShrinkK) {
+        uint4 x[2][2][PA];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = kb + s * 32 + t * 8;
+                load8_parts<PA>(row[i] + k, have[i] && k < k_end, x[s][i]);
+            }
+        __syncthreads();
+        for (int i = tid; i < r * (kShrinkK / 8); i += 128) {
+            uint4 v[PB];
+            int at;
+            if (NN) {
+                const int k = i / (r / 8), q = i % (r / 8) * 8;
+                load8_parts<PB>(M + (int64_t)(kb + k) * r + q, kb + k < k_end, v);
+                at = ((k & 32) + (k & 7) * 4 + (k >> 3 & 3)) * pitch + q * 2;
+            } else {
+                const int q = i / (kShrinkK / 8), k = i % (kShrinkK / 8) * 8;
+                load8_parts<PB>(M + (int64_t)q * a.K + kb + k, kb + k < k_end, v);
+                at = q * pitch + k * 2;
+            }
+#pragma unroll
+            for (int j = 0; j < PB; ++j) *reinterpret_cast<uint4*>(smem + j * part_bytes + at) = v[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                if (n * 8 >= r) break;
+#pragma unroll
+                for (int j = 0; j < PB; ++j) {
+                    uint32_t b[4];
+                    if (NN) {
+                        const int m = lane >> 3, i = lane & 7;
+                        ldmatrix_x4_trans(b, smem + j * part_bytes +
+                                                 (s * 32 + ((i & 1) + 2 * m) * 4 + (i >> 1)) * pitch + n * 16);
+                    } else {
+                        const uint4 v = *reinterpret_cast<const uint4*>(smem + j * part_bytes + (n * 8 + g) * pitch +
+                                                                        (s * 32 + t * 8) * 2);
+                        b[0] = v.x;
+                        b[1] = v.y;
+                        b[2] = v.z;
+                        b[3] = v.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < PA; ++i) {
+                        if (!counts<PA, PB>(i, j)) continue;
+                        const uint4 &lo = x[s][0][i], &hi = x[s][1][i];
+                        mma_bf16(acc[n], lo.x, hi.x, lo.y, hi.y, b[0], b[1]);
+                        mma_bf16(acc[n], lo.z, hi.z, lo.w, hi.w, b[2], b[3]);
+                    }
+                }
+            }
+        }
+    }
+    // the cluster's sums, slice by slice, then the parts
+    __syncthreads();
+    float* mine = reinterpret_cast<float*>(smem);  // [64][r]
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        if (n * 8 >= r) break;
+        const int at = (warp * 16 + g) * r + n * 8 + 2 * t;
+        *reinterpret_cast<float2*>(mine + at) = make_float2(acc[n][0], acc[n][1]);
+        *reinterpret_cast<float2*>(mine + at + 8 * r) = make_float2(acc[n][2], acc[n][3]);
+    }
+    cluster.sync();
+    const int slices = cluster.num_blocks(), rank = cluster.block_rank();
+    const float scale = a.scale[tile.adapter];
+    const int pairs = tile.rows * r / 2;
+    for (int i = rank * 128 + tid; i < pairs; i += 128 * slices) {
+        float2 s = make_float2(0.f, 0.f);
+        for (int q = 0; q < slices; ++q) {
+            const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(mine, q) + 2 * i);
+            s.x += v.x;
+            s.y += v.y;
+        }
+        uint32_t out[PF];
+        split2<PF>(s.x * scale, s.y * scale, out);
+#pragma unroll
+        for (int j = 0; j < PF; ++j)
+            *reinterpret_cast<uint32_t*>(a.out + ((int64_t)j * a.N + tile.pos) * r + 2 * i) = out[j];
+    }
+    cluster.sync();  // the others have read this CTA's sums
+}
+
+// ---------------------------------------------------------------------------
+// expand: out[tok(pos), j] = base[tok, j] (+ out[tok, j]) + sum_q in[pos, q] M_a(q, j)
+//   NN = false: M_a is B_a [J, r] (u -> y);  NN = true: M_a is A_a [r, J] (v -> dx)
+// A CTA has one tile and a span of columns; each warp 16 of the rows, their
+// parts of u in registers throughout.
+// ---------------------------------------------------------------------------
+struct ExpandArgs {
+    const __nv_bfloat16* in;  // [parts][N][r]
+    const void* M;
+    const float* base;        // nullable; may be out
+    float* out;
+    int add_out;              // 1: out already holds the projection
+    int J, r, n_adapters, span;
+    int64_t N;
+    Plan p;
+};
+
+// bytes between rows of r elements so that a half-warp's 8-byte reads (4 rows x
+// 32 bytes) do not collide: 32 above a multiple of 64
+__host__ __device__ constexpr int expand_pitch(int r) { return (2 * r + 31) / 64 * 64 + 32; }
+
+template <typename T, bool NN, int NK>
+__global__ void __launch_bounds__(128) adapter_expand_kernel(const __grid_constant__ ExpandArgs a) {
+    constexpr int PB = Parts<T>::self, PF = Parts<T>::f32;
+    constexpr int R = NK * 16;
+    constexpr int kPitch = NN ? kExpandCols * 2 + 16 : expand_pitch(R);
+    constexpr int kPartBytes = (NN ? R : kExpandCols) * kPitch;
+    extern __shared__ __align__(128) uint8_t smem[];
+    if ((int)blockIdx.x >= *a.p.n_tiles) return;
+    const Tile tile = a.p.tiles[blockIdx.x];
+    const bool none = tile.adapter >= a.n_adapters;
+    // tokens without an adapter: base (and what out holds) alone
+    if (none && (a.add_out ? a.base == nullptr : a.base == a.out)) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int r = a.r, J = a.J;
+    const T* M = static_cast<const T*>(a.M) + (none ? 0 : (int64_t)tile.adapter * r * J);
+    int64_t tok[2];
+    bool have[2];
+    uint32_t u[PF][NK][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int q = warp * 16 + g + 8 * i;
+        have[i] = q < tile.rows;
+        tok[i] = have[i] ? a.p.perm[tile.pos + q] : 0;
+#pragma unroll
+        for (int j = 0; j < PF; ++j)
+#pragma unroll
+            for (int s = 0; s < NK; ++s) {
+                // K in the order (4 t .. 4 t + 3): 8 bytes of a row
+                const int k = s * 16 + 4 * t;
+                uint2 v = make_uint2(0, 0);
+                if (have[i] && k < r && !none)
+                    v = *reinterpret_cast<const uint2*>(a.in + ((int64_t)j * a.N + tile.pos + q) * r + k);
+                u[j][s][i] = v.x;
+                u[j][s][2 + i] = v.y;
+            }
+    }
+    const int j_end = min(J, (int)(blockIdx.y + 1) * a.span);
+    for (int jb = blockIdx.y * a.span; jb < j_end; jb += kExpandCols) {
+        const int cols = min(kExpandCols, j_end - jb);
+        if (!none) {
+            __syncthreads();
+            if (NN) {
+                for (int i = tid; i < R * (kExpandCols / 8); i += 128) {
+                    const int k = i / (kExpandCols / 8), j = i % (kExpandCols / 8) * 8;
+                    uint4 v[PB];
+                    load8_parts<PB>(M + (int64_t)k * J + jb + j, k < r && j < cols, v);
+                    const int at = ((k & ~15) + (k & 3) * 4 + (k >> 2 & 3)) * kPitch + j * 2;
+#pragma unroll
+                    for (int q = 0; q < PB; ++q) *reinterpret_cast<uint4*>(smem + q * kPartBytes + at) = v[q];
+                }
+            } else {
+                for (int i = tid; i < kExpandCols * (R / 8); i += 128) {
+                    const int j = i / (R / 8), k = i % (R / 8) * 8;
+                    uint4 v[PB];
+                    load8_parts<PB>(M + (int64_t)(jb + j) * r + k, k < r && j < cols, v);
+#pragma unroll
+                    for (int q = 0; q < PB; ++q)
+                        *reinterpret_cast<uint4*>(smem + q * kPartBytes + j * kPitch + k * 2) = v[q];
+                }
+            }
+            __syncthreads();
+        }
+#pragma unroll 1
+        for (int n0 = 0; n0 < cols; n0 += 32) {
+            // four column tiles: what is added to, then the products, then the stores
+            float2 add[4][2];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = n0 + n * 8 + 2 * t;
+                    const bool in = have[i] && j < cols;
+                    const int64_t at = tok[i] * J + jb + j;
+                    float2 v = make_float2(0.f, 0.f);
+                    if (in && a.base) v = *reinterpret_cast<const float2*>(a.base + at);
+                    if (in && a.add_out) {
+                        const float2 w = *reinterpret_cast<const float2*>(a.out + at);
+                        v.x += w.x;
+                        v.y += w.y;
+                    }
+                    add[n][i] = v;
+                }
+            float acc[4][4] = {};
+            if (!none) {
+#pragma unroll
+                for (int s = 0; s < NK; ++s) {
+#pragma unroll
+                    for (int q = 0; q < PB; ++q) {
+                        uint32_t b[4][2];
+                        if (NN) {
+                            // two column tiles at a time: (b0, b1) of each
+                            const int m = lane >> 3, i = lane & 7;
+                            const uint8_t* at = smem + q * kPartBytes +
+                                                (s * 16 + ((i & 1) + 2 * (m & 1)) * 4 + (i >> 1)) * kPitch +
+                                                (n0 + (m >> 1) * 8) * 2;
+                            uint32_t v[4];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                ldmatrix_x4_trans(v, at + h * 32);
+                                b[2 * h][0] = v[0];
+                                b[2 * h][1] = v[1];
+                                b[2 * h + 1][0] = v[2];
+                                b[2 * h + 1][1] = v[3];
+                            }
+                        } else {
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                const uint2 v = *reinterpret_cast<const uint2*>(
+                                    smem + q * kPartBytes + (n0 + n * 8 + g) * kPitch + (s * 16 + 4 * t) * 2);
+                                b[n][0] = v.x;
+                                b[n][1] = v.y;
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < PF; ++j) {
+                            if (!counts<PF, PB>(j, q)) continue;
+#pragma unroll
+                            for (int n = 0; n < 4; ++n)
+                                mma_bf16(acc[n], u[j][s][0], u[j][s][1], u[j][s][2], u[j][s][3], b[n][0], b[n][1]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = n0 + n * 8 + 2 * t;
+                    if (have[i] && j < cols)
+                        *reinterpret_cast<float2*>(a.out + tok[i] * J + jb + j) =
+                            make_float2(add[n][i].x + acc[n][2 * i], add[n][i].y + acc[n][2 * i + 1]);
+                }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// grad: G_a(q, j) = sum over adapter a's tokens of in[pos, q] Z[tok(pos), j]
+//   TRANS = false: dA_a [r, J] from v and x;  TRANS = true: dB_a [J, r] from u and dy
+// A CTA has one adapter, 128 columns and one split of the tokens; each warp 16
+// of the columns and all ranks.  Both operands have K (the tokens) as their
+// slow axis and come through shared memory by transposing loads.
+// ---------------------------------------------------------------------------
+struct GradArgs {
+    const __nv_bfloat16* in;  // [parts][N][r]
+    const void* Z;
+    float* out;               // [n_adapters][r J], or partial sums [splits][n_adapters][r J]
+    int J, r, n_adapters;
+    int64_t N;
+    Plan p;
+};
+
+template <typename T, typename TZ, bool TRANS, int MT>
+__global__ void __launch_bounds__(256) adapter_grad_kernel(const __grid_constant__ GradArgs a) {
+    constexpr int PZ = act_parts<TZ, T>(), PF = Parts<T>::f32;
+    constexpr int kInPitch = MT * 32 + 16, kZPitch = kGradCols * 2 + 16;
+    constexpr int kInPart = kGradRows * kInPitch, kZPart = kGradRows * kZPitch;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* in_s = smem;
+    uint8_t* z_s = smem + PF * kInPart;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int adapter = blockIdx.y, splits = gridDim.z, split = blockIdx.z;
+    const int r = a.r, J = a.J, jb = blockIdx.x * kGradCols;
+    const int seg0 = a.p.seg[adapter], seg1 = a.p.seg[adapter + 1];
+    const int chunks = (seg1 - seg0 + kGradRows - 1) / kGradRows;
+    const int c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
+    const TZ* Z = static_cast<const TZ*>(a.Z);
+    float acc[MT][2][4] = {};
+    // this thread's elements of a chunk: of Z, 8 columns of two rows; of in, 8 ranks of some rows
+    const int zc = tid & 15, zr = tid >> 4;
+    uint4 z[2][PZ];
+    auto load_z = [&](int c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int pos = seg0 + c * kGradRows + zr + 16 * h;
+            const bool in = pos < seg1 && jb + zc * 8 < J;
+            const int64_t tok = in ? a.p.perm[pos] : 0;
+            load8_parts<PZ>(Z + tok * J + jb + zc * 8, in, z[h]);
+        }
+    };
+    if (c0 < c1) load_z(c0);
+    for (int c = c0; c < c1; ++c) {
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < PZ; ++q)
+                *reinterpret_cast<uint4*>(z_s + q * kZPart + (zr + 16 * h) * kZPitch + zc * 16) = z[h][q];
+        for (int i = tid; i < kGradRows * MT * 2; i += 256) {
+            const int row = i / (MT * 2), q = i % (MT * 2) * 8, pos = seg0 + c * kGradRows + row;
+#pragma unroll
+            for (int j = 0; j < PF; ++j) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (pos < seg1 && q < r) v = *reinterpret_cast<const uint4*>(a.in + ((int64_t)j * a.N + pos) * r + q);
+                *reinterpret_cast<uint4*>(in_s + j * kInPart + row * kInPitch + q * 2) = v;
+            }
+        }
+        __syncthreads();
+        if (c + 1 < c1) load_z(c + 1);
+#pragma unroll
+        for (int s = 0; s < kGradRows / 16; ++s) {
+            const int m = lane >> 3, i = lane & 7;
+            // B: (k 0-7, n 0-7), (k 8-15, n 0-7), then the next column tile
+            uint32_t b[PZ][4];
+#pragma unroll
+            for (int q = 0; q < PZ; ++q)
+                ldmatrix_x4_trans(b[q], z_s + q * kZPart + (s * 16 + (m & 1) * 8 + i) * kZPitch +
+                                            (warp * 16 + (m >> 1) * 8) * 2);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int j = 0; j < PF; ++j) {
+                    // A: (m 0-7, k 0-7), (m 8-15, k 0-7), (m 0-7, k 8-15), (m 8-15, k 8-15)
+                    uint32_t v[4];
+                    ldmatrix_x4_trans(v, in_s + j * kInPart + (s * 16 + (m >> 1) * 8 + i) * kInPitch +
+                                             (mt * 16 + (m & 1) * 8) * 2);
+#pragma unroll
+                    for (int q = 0; q < PZ; ++q) {
+                        if (!counts<PF, PZ>(j, q)) continue;
+                        mma_bf16(acc[mt][0], v[0], v[1], v[2], v[3], b[q][0], b[q][1]);
+                        mma_bf16(acc[mt][1], v[0], v[1], v[2], v[3], b[q][2], b[q][3]);
+                    }
+                }
+            }
+        }
+    }
+    float* out = a.out + ((int64_t)split * a.n_adapters + adapter) * r * J;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int q = mt * 16 + g + 8 * h, j = jb + warp * 16 + n * 8 + 2 * t;
+                if (q >= r || j >= J) continue;
+                const float v0 = acc[mt][n][2 * h], v1 = acc[mt][n][2 * h + 1];
+                if (TRANS) {
+                    out[(int64_t)j * r + q] = v0;
+                    out[(int64_t)(j + 1) * r + q] = v1;
+                } else {
+                    *reinterpret_cast<float2*>(out + (int64_t)q * J + j) = make_float2(v0, v1);
+                }
+            }
+}
+
+__global__ void __launch_bounds__(256) adapter_reduce_kernel(const float4* part, int splits, int64_t n4, float4* out) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+        float4 s = part[i];
+        for (int q = 1; q < splits; ++q) {
+            const float4 v = part[(int64_t)q * n4 + i];
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        out[i] = s;
+    }
+}
+
+// dy as two bf16 parts, the operands of W^T dy
+__global__ void __launch_bounds__(256) adapter_split_kernel(const float* v, int64_t n, __nv_bfloat16* hi,
+                                                            __nv_bfloat16* lo) {
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
+        uint4 p[2];
+        load8_parts<2>(v + i, true, p);
+        *reinterpret_cast<uint4*>(hi + i) = p[0];
+        *reinterpret_cast<uint4*>(lo + i) = p[1];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A few tokens: u's partial sums per token and K slice, then y
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ void load8_f32(const T* p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8_f32<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __bfloat1622float2(h[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+template <>
+__device__ __forceinline__ void load8_f32<float>(const float* p, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(p + 4 * i);
+        v[4 * i] = f.x;
+        v[4 * i + 1] = f.y;
+        v[4 * i + 2] = f.z;
+        v[4 * i + 3] = f.w;
+    }
+}
+
+// CTA (slice, token): part[slice][token][q] over the slice's K, warp w the ranks w, w + 4, ...
+template <typename T>
+__global__ void __launch_bounds__(128)
+    adapter_few_shrink_kernel(const T* x, const T* A, const float* scale, const int32_t* ids, int N, int K, int r,
+                              int n_adapters, int slice, float* part, unsigned long long* counters) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t = blockIdx.y;
+    if (blockIdx.x == 0 && t == 0 && tid < CNT_COUNT) counters[tid] = 0ull;
+    const int id = ids[t];
+    if (id < 0 || id >= n_adapters) return;
+    const int k0 = blockIdx.x * slice, k1 = min(K, k0 + slice);
+    const T* M = A + (int64_t)id * r * K;
+    float* out = part + ((int64_t)blockIdx.x * N + t) * r;
+    for (int q0 = warp; q0 < r; q0 += 16) {  // four ranks at a time
+        float acc[4] = {};
+        for (int k = k0 + lane * 8; k < k1; k += 256) {
+            float xv[8];
+            load8_f32<T>(x + (int64_t)t * K + k, xv);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int q = q0 + 4 * i;
+                if (q < r) {
+                    float m[8];
+                    load8_f32<T>(M + (int64_t)q * K + k, m);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[i] = fmaf(xv[e], m[e], acc[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float s = acc[i];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0 && q0 + 4 * i < r) out[q0 + 4 * i] = s * scale[id];
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(128)
+    adapter_few_expand_kernel(const float* part, int slices, const T* B, const int32_t* ids, int N, int J, int r,
+                              int n_adapters, const float* base, float* out, int add_out,
+                              unsigned long long* counters) {
+    __shared__ float u[kMaxAdapterRank];
+    const int tid = threadIdx.x, t = blockIdx.y, j = blockIdx.x * 128 + tid;
+    const int id = ids[t];
+    const bool none = id < 0 || id >= n_adapters;
+    const int64_t at = (int64_t)t * J + j;
+    float s = 0.f;
+    if (j < J && base) s = base[at];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (j < J && add_out) s += out[at];
+    if (!none) {
+        for (int q = tid; q < r; q += 128) {
+            float v = 0.f;
+            for (int i = 0; i < slices; ++i) v += part[((int64_t)i * N + t) * r + q];
+            u[q] = v;
+        }
+        __syncthreads();
+        if (j < J) {
+            const T* row = B + ((int64_t)id * J + j) * r;
+            float acc = 0.f;
+#pragma unroll 4
+            for (int q = 0; q < r; q += 8) {
+                float m[8];
+                load8_f32<T>(row + q, m);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc = fmaf(u[q + e], m[e], acc);
+            }
+            s += acc;
+        }
+    } else if (id != -1 && blockIdx.x == 0 && tid == 0) {
+        atomicOr(counters + CNT_DEVICE_ERROR, (unsigned long long)DEVERR_BOUNDS);
+    }
+    if (j < J) out[at] = s;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// an upper bound of the tiles: every adapter (and the tokens without one) may end in a part of a tile
+int64_t tile_bound(const moe_adapter_params& p) {
+    return p.N / kRows + std::min<int64_t>(p.n_adapters + 1, p.N);
+}
+
+// K slices of a shrink: enough CTAs for two waves of the likely tiles, at least 512 of K each
+int shrink_slices(const moe_adapter_params& p, int K) {
+    const int64_t tiles = p.N / kRows + (std::min<int64_t>(p.n_adapters, p.N) + 1) / 2;
+    const int64_t want = (4 * (int64_t)num_sms() + tiles - 1) / std::max<int64_t>(tiles, 1);
+    int s = 1;
+    while (s * 2 <= kMaxSlices && s * 2 <= want && K / (s * 2) >= 512) s *= 2;
+    return s;
+}
+
+int few_slices(int64_t N, int K) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>({16, 2 * num_sms() / std::max<int64_t>(N, 1), K / 256}));
+}
+
+// token splits of a grad, whose partial sums a reduction adds in order
+int grad_splits(const moe_adapter_params& p, int J) {
+    const int64_t ctas = (int64_t)((J + kGradCols - 1) / kGradCols) * p.n_adapters;
+    const int64_t want = (2 * (int64_t)num_sms() + ctas - 1) / ctas;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, want, p.N / 256}));
+}
+
+struct Layout {
+    size_t counters, perm, seg, tiles, one_group, u, v, hi, lo, part, total;
+};
+
+Layout layout_of(const moe_adapter_params& p, bool with_W, bool backward) {
+    const size_t N = (size_t)p.N, r = (size_t)p.r;
+    const int parts = p.dtype == MOE_BF16 ? Parts<__nv_bfloat16>::f32 : Parts<float>::f32;
+    Layout L{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = up256(off + bytes);
+        return o;
+    };
+    L.counters = take(CNT_COUNT * 8);
+    L.perm = take(N * 4);
+    L.seg = take(((size_t)p.n_adapters + 2) * 4);
+    L.one_group = take(5 * 4);  // and the number of tiles
+    L.tiles = take((size_t)tile_bound(p) * sizeof(Tile));
+    // u as parts, or (a few tokens) as partial sums
+    L.u = take(std::max(N * r * 2 * parts, N <= kFewN ? 16 * N * r * 4 : 0));
+    if (backward) {
+        L.v = take(N * r * 2 * parts);
+        if (with_W && p.dtype == MOE_BF16) {
+            L.hi = take(N * (size_t)p.d_out * 2);
+            L.lo = take(N * (size_t)p.d_out * 2);
+        }
+        const int sa = grad_splits(p, p.d_in), sb = grad_splits(p, p.d_out);
+        const size_t pa = sa > 1 ? (size_t)sa * p.d_in : 0, pb = sb > 1 ? (size_t)sb * p.d_out : 0;
+        L.part = take(std::max(pa, pb) * (size_t)p.n_adapters * r * 4);
+    }
+    L.total = off;
+    return L;
+}
+
+Plan plan_of(const Layout& L, char* ws) {
+    Plan p;
+    p.counters = reinterpret_cast<unsigned long long*>(ws + L.counters);
+    p.perm = reinterpret_cast<int32_t*>(ws + L.perm);
+    p.seg = reinterpret_cast<int32_t*>(ws + L.seg);
+    p.one_group = reinterpret_cast<int32_t*>(ws + L.one_group);
+    p.n_tiles = p.one_group + 4;
+    p.tiles = reinterpret_cast<Tile*>(ws + L.tiles);
+    return p;
+}
+
+cudaError_t launch_plan(const moe_adapter_params& p, const int32_t* ids, const Plan& plan, cudaStream_t st) {
+    const size_t smem = (size_t)(34 * (p.n_adapters + 2)) * 4;
+    cudaError_t e = allow_smem_once<adapter_plan_kernel>(34 * (kMaxAdapters + 2) * 4);
+    if (e != cudaSuccess) return e;
+    adapter_plan_kernel<<<1, 1024, smem, st>>>(ids, (int)p.N, p.n_adapters, plan);
+    return cudaGetLastError();
+}
+
+template <typename T, typename TA, bool NN, int NQ>
+cudaError_t launch_shrink_q(const moe_adapter_params& p, ShrinkArgs a, cudaStream_t st) {
+    constexpr auto kern = adapter_shrink_kernel<T, TA, NN, NQ>;
+    const int slices = shrink_slices(p, a.K);
+    a.slice = ((a.K + slices - 1) / slices + kShrinkK - 1) / kShrinkK * kShrinkK;
+    const size_t staged = (size_t)Parts<T>::self * (NN ? (size_t)kShrinkK * (p.r * 2 + 16) : (size_t)p.r * (kShrinkK * 2 + 64));
+    const size_t smem = std::max(staged, (size_t)kRows * p.r * 4);
+    constexpr size_t most = std::max((size_t)Parts<T>::self * (NN ? kShrinkK * (NQ * 16 + 16) : NQ * 8 * (kShrinkK * 2 + 64)),
+                                     (size_t)kRows * NQ * 8 * 4);
+    cudaError_t e = allow_smem_once<kern>(most);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tile_bound(p), (unsigned)slices, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = (unsigned)slices;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T, typename TA, bool NN>
+cudaError_t launch_shrink(const moe_adapter_params& p, const TA* X, const T* M, const float* scale, int K,
+                          __nv_bfloat16* out, const Plan& plan, cudaStream_t st) {
+    ShrinkArgs a{};
+    a.X = X;
+    a.M = M;
+    a.scale = scale;
+    a.K = K;
+    a.r = p.r;
+    a.n_adapters = p.n_adapters;
+    a.N = p.N;
+    a.out = out;
+    a.p = plan;
+    if (p.r <= 16) return launch_shrink_q<T, TA, NN, 2>(p, a, st);
+    if (p.r <= 32) return launch_shrink_q<T, TA, NN, 4>(p, a, st);
+    if (p.r <= 64) return launch_shrink_q<T, TA, NN, 8>(p, a, st);
+    return launch_shrink_q<T, TA, NN, 16>(p, a, st);
+}
+
+template <typename T, bool NN, int NK>
+cudaError_t launch_expand_k(const moe_adapter_params& p, ExpandArgs a, cudaStream_t st) {
+    constexpr auto kern = adapter_expand_kernel<T, NN, NK>;
+    constexpr size_t smem = (size_t)Parts<T>::self * (NN ? NK * 16 * (kExpandCols * 2 + 16) : kExpandCols * expand_pitch(NK * 16));
+    static_assert(smem <= 232448, "shared memory per CTA");
+    cudaError_t e = allow_smem_once<kern>(smem);
+    if (e != cudaSuccess) return e;
+    // columns of a CTA: as many as leave two waves of CTAs
+    const int64_t tiles = p.N / kRows + 1;
+    a.span = 4 * kExpandCols;
+    while (a.span > kExpandCols && tiles * ((a.J + a.span - 1) / a.span) < 2 * num_sms()) a.span /= 2;
+    const dim3 grid((unsigned)tile_bound(p), (unsigned)((a.J + a.span - 1) / a.span), 1);
+    kern<<<grid, 128, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, bool NN>
+cudaError_t launch_expand(const moe_adapter_params& p, const __nv_bfloat16* in, const T* M, int J, const float* base,
+                          float* out, int add_out, const Plan& plan, cudaStream_t st) {
+    ExpandArgs a{};
+    a.in = in;
+    a.M = M;
+    a.base = base;
+    a.out = out;
+    a.add_out = add_out;
+    a.J = J;
+    a.r = p.r;
+    a.n_adapters = p.n_adapters;
+    a.N = p.N;
+    a.p = plan;
+    if (p.r <= 16) return launch_expand_k<T, NN, 1>(p, a, st);
+    if (p.r <= 32) return launch_expand_k<T, NN, 2>(p, a, st);
+    if (p.r <= 64) return launch_expand_k<T, NN, 4>(p, a, st);
+    return launch_expand_k<T, NN, 8>(p, a, st);
+}
+
+template <typename T, typename TZ, bool TRANS, int MT>
+cudaError_t launch_grad_m(const GradArgs& a, dim3 grid, cudaStream_t st) {
+    constexpr auto kern = adapter_grad_kernel<T, TZ, TRANS, MT>;
+    constexpr size_t smem = (size_t)kGradRows * (Parts<T>::f32 * (MT * 32 + 16) + act_parts<TZ, T>() * (kGradCols * 2 + 16));
+    cudaError_t e = allow_smem_once<kern>(smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, 256, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, typename TZ, bool TRANS>
+cudaError_t launch_grad(const moe_adapter_params& p, const __nv_bfloat16* in, const TZ* Z, int J, float* out,
+                        float* part, const Plan& plan, cudaStream_t st) {
+    const int splits = grad_splits(p, J);
+    GradArgs a{};
+    a.in = in;
+    a.Z = Z;
+    a.out = splits > 1 ? part : out;
+    a.J = J;
+    a.r = p.r;
+    a.n_adapters = p.n_adapters;
+    a.N = p.N;
+    a.p = plan;
+    const dim3 grid((unsigned)((J + kGradCols - 1) / kGradCols), (unsigned)p.n_adapters, (unsigned)splits);
+    cudaError_t e = p.r <= 16   ? launch_grad_m<T, TZ, TRANS, 1>(a, grid, st)
+                    : p.r <= 32 ? launch_grad_m<T, TZ, TRANS, 2>(a, grid, st)
+                    : p.r <= 64 ? launch_grad_m<T, TZ, TRANS, 4>(a, grid, st)
+                                : launch_grad_m<T, TZ, TRANS, 8>(a, grid, st);
+    if (e != cudaSuccess || splits == 1) return e;
+    const int64_t n4 = (int64_t)p.n_adapters * p.r * J / 4;
+    adapter_reduce_kernel<<<(unsigned)min64((n4 + 255) / 256, (int64_t)num_sms() * 8), 256, 0, st>>>(
+        reinterpret_cast<const float4*>(part), splits, n4, reinterpret_cast<float4*>(out));
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t forward(const moe_adapter_params& p, const T* x, const T* W, const T* A, const T* B, const float* scale,
+                    const int32_t* ids, const float* base, float* y, char* ws, cudaStream_t st) {
+    const Layout L = layout_of(p, W != nullptr, false);
+    const Plan plan = plan_of(L, ws);
+    const bool few = p.N <= kFewN;
+    const int slices = few_slices(p.N, p.d_in);
+    float* part = reinterpret_cast<float*>(ws + L.u);
+    __nv_bfloat16* u = reinterpret_cast<__nv_bfloat16*>(ws + L.u);
+    cudaError_t e;
+    if (few) {
+        const int slice = ((p.d_in + slices - 1) / slices + 7) / 8 * 8;
+        adapter_few_shrink_kernel<T><<<dim3(slices, (unsigned)p.N), 128, 0, st>>>(
+            x, A, scale, ids, (int)p.N, p.d_in, p.r, p.n_adapters, slice, part, plan.counters);
+        e = cudaGetLastError();
+    } else {
+        e = launch_plan(p, ids, plan, st);
+        if (e == cudaSuccess) e = launch_shrink<T, T, false>(p, x, A, scale, p.d_in, u, plan, st);
+    }
+    if (e != cudaSuccess) return e;
+    if (W) {
+        int status = MOE_OK;
+        if (sizeof(T) == 2) e = launch_tc_dense(p.N, p.d_out, p.d_in, x, W, y, plan.counters, st, &status);
+        else
+            e = launch_simt_dense(p.N, p.d_out, p.d_in, reinterpret_cast<const float*>(x), p.d_in, 1,
+                                  reinterpret_cast<const float*>(W), p.d_in, 1, y, p.d_out, st);
+        if (e != cudaSuccess) return e;
+    }
+    if (!few) return launch_expand<T, false>(p, u, B, p.d_out, base, y, W != nullptr, plan, st);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.d_out + 127) / 128), (unsigned)p.N, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.stream = st;
+    // set up while the shrink runs (not behind the projection, which does not say when it is done)
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = W ? 0 : 1;
+    e = cudaLaunchKernelEx(&cfg, adapter_few_expand_kernel<T>, (const float*)part, slices, B, ids, (int)p.N, p.d_out,
+                           p.r, p.n_adapters, base, y, (int)(W != nullptr), plan.counters);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t backward(const moe_adapter_params& p, const T* x, const T* W, const T* A, const T* B, const float* scale,
+                     const int32_t* ids, const float* dy, const float* dx_base, float* dx, float* dA, float* dB,
+                     char* ws, cudaStream_t st) {
+    const Layout L = layout_of(p, W != nullptr, true);
+    const Plan plan = plan_of(L, ws);
+    __nv_bfloat16* u = reinterpret_cast<__nv_bfloat16*>(ws + L.u);
+    __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(ws + L.v);
+    float* part = reinterpret_cast<float*>(ws + L.part);
+    cudaError_t e = launch_plan(p, ids, plan, st);
+    if (e == cudaSuccess) e = launch_shrink<T, T, false>(p, x, A, scale, p.d_in, u, plan, st);
+    if (e == cudaSuccess) e = launch_shrink<T, float, true>(p, dy, B, scale, p.d_out, v, plan, st);
+    if (e != cudaSuccess) return e;
+    if (W && sizeof(T) == 2) {
+        __nv_bfloat16* hi = reinterpret_cast<__nv_bfloat16*>(ws + L.hi);
+        __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(ws + L.lo);
+        const int64_t n = p.N * (int64_t)p.d_out;
+        adapter_split_kernel<<<(unsigned)min64((n / 8 + 255) / 256, (int64_t)num_sms() * 8), 256, 0, st>>>(dy, n, hi, lo);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        moe_params q{};
+        q.N = p.N;
+        q.E_r = 1;
+        q.k = 1;
+        q.dtype = MOE_BF16;
+        int status = MOE_OK;
+        e = launch_tc_store_bmn(q, p.d_in, p.d_out, hi, p.d_out, W, lo, p.d_out, W, plan.one_group, plan.one_group + 2,
+                                dx, plan.counters, st, &status);
+    } else if (W) {
+        e = launch_simt_dense(p.N, p.d_in, p.d_out, dy, p.d_out, 1, reinterpret_cast<const float*>(W), 1, p.d_in, dx,
+                              p.d_in, st);
+    }
+    if (e == cudaSuccess) e = launch_expand<T, true>(p, v, A, p.d_in, dx_base, dx, W != nullptr, plan, st);
+    if (e == cudaSuccess) e = launch_grad<T, T, false>(p, v, x, p.d_in, dA, part, plan, st);
+    if (e == cudaSuccess) e = launch_grad<T, float, true>(p, u, dy, p.d_out, dB, part, plan, st);
+    return e;
+}
+
+// what a call with a projection needs besides
+moe_status check_projection(const moe_adapter_params* p, const void* W) {
+    if (W && p->dtype == MOE_F32 && p->N > (int64_t)65535 * 64) {
+        record_error("moe_adapter: at most 65535 * 64 tokens through an fp32 projection");
+        return MOE_ERR_UNSUPPORTED;
+    }
+    return MOE_OK;
+}
+
+moe_status check(const moe_adapter_params* p) {
+    if (!p) return MOE_ERR_INVALID_ARG;
+    if (p->N < 0 || p->d_in < 1 || p->d_out < 1 || p->n_adapters < 1 || p->r < 1) return MOE_ERR_INVALID_ARG;
+    if (p->dtype != MOE_F32 && p->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (p->d_in % 8 || p->d_out % 8 || p->r % 8) {
+        record_error("moe_adapter: d_in, d_out and r must be multiples of 8");
+        return MOE_ERR_UNSUPPORTED;
+    }
+    if (p->r > kMaxAdapterRank || p->n_adapters > kMaxAdapters || p->N >= (int64_t)1 << 30) {
+        record_error("moe_adapter: at most rank 128, 1024 adapters and 2^30 - 1 tokens");
+        return MOE_ERR_UNSUPPORTED;
+    }
+    return MOE_OK;
+}
+
+bool al16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
+
+moe_status status_of(cudaError_t e, const char* where) {
+    if (e == cudaSuccess) return MOE_OK;
+    char buf[160];
+    snprintf(buf, sizeof(buf), "%s: %s (%d)", where, cudaGetErrorString(e), (int)e);
+    record_error(buf);
+    return MOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_adapter_workspace_size(const moe_adapter_params* p, int with_W, size_t* bytes) {
+    const moe_status s = check(p);
+    if (s != MOE_OK) return s;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = layout_of(*p, with_W != 0, false).total;
+    return MOE_OK;
+}
+
+moe_status moe_adapter_backward_workspace_size(const moe_adapter_params* p, int with_W, size_t* bytes) {
+    const moe_status s = check(p);
+    if (s != MOE_OK) return s;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = layout_of(*p, with_W != 0, true).total;
+    return MOE_OK;
+}
+
+moe_status moe_adapter_forward(const moe_adapter_params* p, const void* x, const void* W, const void* A, const void* B,
+                               const float* scale, const int32_t* ids, const float* base, float* y, void* ws,
+                               moe_stream_t stream) {
+    moe_status s = check(p);
+    if (s == MOE_OK) s = check_projection(p, W);
+    if (s != MOE_OK) return s;
+    if (!ws || !al16(ws)) return MOE_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    (void)cudaGetLastError();
+    char* w = static_cast<char*>(ws);
+    if (p->N == 0)
+        return status_of(cudaMemsetAsync(w + layout_of(*p, false, false).counters, 0, CNT_COUNT * 8, st),
+                         "moe_adapter_forward memset");
+    if (!x || !A || !B || !scale || !ids || !y) return MOE_ERR_INVALID_ARG;
+    if (!al16(x) || !al16(W) || !al16(A) || !al16(B) || !al16(base) || !al16(y)) return MOE_ERR_INVALID_ARG;
+    if (W && base == y) return MOE_ERR_INVALID_ARG;  // the projection is written before base is added
+    const cudaError_t e =
+        p->dtype == MOE_BF16
+            ? forward(*p, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(W),
+                      static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, ids, base, y, w, st)
+            : forward(*p, static_cast<const float*>(x), static_cast<const float*>(W), static_cast<const float*>(A),
+                      static_cast<const float*>(B), scale, ids, base, y, w, st);
+    return status_of(e, "moe_adapter_forward");
+}
+
+moe_status moe_adapter_backward(const moe_adapter_params* p, const void* x, const void* W, const void* A, const void* B,
+                                const float* scale, const int32_t* ids, const float* dy, const float* dx_base,
+                                float* dx, float* dA, float* dB, void* ws, moe_stream_t stream) {
+    moe_status s = check(p);
+    if (s == MOE_OK) s = check_projection(p, W);
+    if (s != MOE_OK) return s;
+    if (!ws || !al16(ws)) return MOE_ERR_WORKSPACE;
+    if (!dA || !dB || !al16(dA) || !al16(dB)) return MOE_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    (void)cudaGetLastError();
+    char* w = static_cast<char*>(ws);
+    if (p->N == 0) {
+        const size_t n = (size_t)p->n_adapters * p->r * 4;
+        cudaError_t e = cudaMemsetAsync(w + layout_of(*p, false, true).counters, 0, CNT_COUNT * 8, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dA, 0, n * p->d_in, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, n * p->d_out, st);
+        return status_of(e, "moe_adapter_backward memset");
+    }
+    if (!x || !A || !B || !scale || !ids || !dy || !dx) return MOE_ERR_INVALID_ARG;
+    if (!al16(x) || !al16(W) || !al16(A) || !al16(B) || !al16(dy) || !al16(dx_base) || !al16(dx))
+        return MOE_ERR_INVALID_ARG;
+    if (W && dx_base == dx) return MOE_ERR_INVALID_ARG;
+    const cudaError_t e =
+        p->dtype == MOE_BF16
+            ? backward(*p, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(W),
+                       static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, ids, dy,
+                       dx_base, dx, dA, dB, w, st)
+            : backward(*p, static_cast<const float*>(x), static_cast<const float*>(W), static_cast<const float*>(A),
+                       static_cast<const float*>(B), scale, ids, dy, dx_base, dx, dA, dB, w, st);
+    return status_of(e, "moe_adapter_backward");
+}
+
+moe_status moe_adapter_check(const moe_adapter_params* p, const void* ws, moe_stream_t stream) {
+    const moe_status s = check(p);
+    if (s != MOE_OK) return s;
+    if (!ws) return MOE_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    unsigned long long cnt[CNT_COUNT];
+    cudaError_t e = cudaMemcpyAsync(cnt, static_cast<const char*>(ws) + layout_of(*p, false, false).counters,
+                                    sizeof(cnt), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess) return status_of(e, "moe_adapter_check");
+    if (cnt[CNT_DEVICE_ERROR] & DEVERR_TIMEOUT) return MOE_ERR_TIMEOUT;
+    if (cnt[CNT_DEVICE_ERROR] & DEVERR_BOUNDS) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+}  // extern "C"

@@ -990,6 +990,12 @@ bool offsets_valid(const moe_params& p, const int32_t* o) {
 }
 
 }  // namespace
+
+cudaError_t launch_simt_dense(int64_t M, int64_t N, int64_t K, const float* A, int64_t sam, int64_t sak, const float* B,
+                              int64_t sbn, int64_t sbk, float* C, int64_t ldc, cudaStream_t st) {
+    return simt_gemm<float, float>(M, N, K, A, sam, sak, B, sbn, sbk, C, ldc, st);
+}
+
 }  // namespace moe
 
 using namespace moe;

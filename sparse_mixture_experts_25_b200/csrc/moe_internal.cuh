@@ -215,6 +215,14 @@ cudaError_t launch_simt_down(const moe_params& p, int mode, const void* h, const
                              const ExpertWeights& W, const int32_t* slot_token,
                              const float* slot_w, float* Y, float* H_out, cudaStream_t st);
 
+// backward.cu: C[m, n] = sum_k A[m sam + k sak] B[n sbn + k sbk] on the CUDA cores
+cudaError_t launch_simt_dense(int64_t M, int64_t N, int64_t K, const float* A, int64_t sam, int64_t sak, const float* B,
+                              int64_t sbn, int64_t sbk, float* C, int64_t ldc, cudaStream_t st);
+
+// adapters.cu
+constexpr int kMaxAdapters = 1024;
+constexpr int kMaxAdapterRank = 128;
+
 // few.cu: the whole layer for at most kFewMaxTokens tokens.  Its part of the
 // workspace follows the layer's own regions.
 struct FewLayout {
