@@ -695,6 +695,43 @@ MOE_API moe_status moe_adapter_backward(const moe_adapter_params* p, const void*
 MOE_API moe_status moe_adapter_check(const moe_adapter_params* p, const void* ws, moe_stream_t stream);
 
 /*
+ * Dropout of the layer's output in front of the residual sum, with a mask that
+ * is a function of a counter and never stored:
+ *   forward   out = residual + m Y / (1 - rate)
+ *   backward  dY  = m dout / (1 - rate)   (the gradient of residual is dout)
+ * m(t, c) = [word(t, c) >= min(round(rate 2^32), 2^32 - 1)], word(t, c) word c mod 4 of
+ * Philox4x32-10 (Salmon, Moraes, Dror and Shaw, 2011) under the 64-bit key
+ * `seed` at the counter whose low 64 bits are ((row0 + t) d + c) / 4 and whose
+ * high 64 bits are `offset` (+ *step).  row0 is the row that the call's first
+ * token has in the whole batch, so that the shards of a batch draw what one
+ * GPU with all of it would.  step (device uint64, nullable, 8-byte aligned) is
+ * read by the kernel: a captured call draws another mask at each replay when
+ * the program counts it up in between.  A dropped element adds 0 even where Y
+ * or dout is not finite.
+ *   Y, dY [N, d] fp32 (moe_forward's output, moe_backward's upstream gradient)
+ *   residual (nullable), out, dout [N, d] of params.dtype
+ * out may be residual, and for fp32 calls Y (backward: dY may be dout).  Sums
+ * are fp32, rounded once to dtype.  0 <= rate < 1 (0 draws nothing); d a
+ * multiple of 8, N d < 2^42 - 2048, (row0 + N) d <= 2^62
+ * (MOE_ERR_UNSUPPORTED); pointers 16-byte aligned.  No workspace, asynchronous
+ * on `stream`.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
+ */
+typedef struct moe_dropout_params {
+    int64_t N;        /* tokens                                                */
+    int64_t row0;     /* row of the first token in the whole batch, >= 0       */
+    uint64_t seed;    /* key of the generator                                  */
+    uint64_t offset;  /* call number: high half of the counter                 */
+    double rate;      /* probability that an element is dropped                */
+    int32_t d;        /* width                                                 */
+    int32_t dtype;    /* moe_dtype of residual, out and dout                   */
+} moe_dropout_params;
+
+MOE_API moe_status moe_dropout_forward(const moe_dropout_params* p, const float* Y, const void* residual, void* out,
+                                       const uint64_t* step, moe_stream_t stream);
+MOE_API moe_status moe_dropout_backward(const moe_dropout_params* p, const void* dout, float* dY,
+                                        const uint64_t* step, moe_stream_t stream);
+
+/*
  * Self-test of the library's bounded device waits (no counterpart on the
  * pages).  Launches one CTA that waits on a shared-memory mbarrier nothing
  * ever arrives on, with the same bounded-wait routine the tensor-core GEMMs

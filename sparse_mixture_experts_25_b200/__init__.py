@@ -29,6 +29,7 @@ __all__ = [
     "moe_soft_check",
     "AdapterParams", "adapter_params", "moe_adapter_workspace_size", "moe_adapter_backward_workspace_size",
     "moe_adapter_forward", "moe_adapter_backward", "moe_adapter_check",
+    "DropoutParams", "dropout_params", "moe_dropout_forward", "moe_dropout_backward",
     "workspace_views", "HEADER",
 ]
 
@@ -81,6 +82,20 @@ def adapter_params(N, d_in, d_out, n_adapters, r, dtype=None) -> AdapterParams:
     """Low-rank adapters of many requests (see moe_adapter_forward in the header)."""
     return AdapterParams(int(N), int(d_in), int(d_out), int(n_adapters), int(r),
                          int(MOE_BF16 if dtype is None else dtype), 0)
+
+
+class DropoutParams(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("row0", ctypes.c_int64), ("seed", ctypes.c_uint64),
+                ("offset", ctypes.c_uint64), ("rate", ctypes.c_double), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+def dropout_params(N, d, rate, seed=0, offset=0, row0=0, dtype=None) -> DropoutParams:
+    """Dropout of a layer's output (see moe_dropout_forward in the header);
+    seed and offset are taken modulo 2^64."""
+    m = (1 << 64) - 1
+    return DropoutParams(int(N), int(row0), int(seed) & m, int(offset) & m, float(rate), int(d),
+                         int(MOE_BF16 if dtype is None else dtype))
 
 
 class Stats(ctypes.Structure):
@@ -161,6 +176,9 @@ def lib():
         L.moe_adapter_forward.argtypes = [ap] + [_P] * 10
         L.moe_adapter_backward.argtypes = [ap] + [_P] * 13
         L.moe_adapter_check.argtypes = [ap, _P, _P]
+        dp = ctypes.POINTER(DropoutParams)
+        L.moe_dropout_forward.argtypes = [dp, _P, _P, _P, _P, _P]
+        L.moe_dropout_backward.argtypes = [dp, _P, _P, _P, _P]
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         L.moe_status_string.argtypes = [ctypes.c_int]
@@ -174,7 +192,7 @@ def lib():
                      "moe_backward_workspace_size", "moe_backward", "moe_backward_check",
                      "moe_few_workspace_size", "moe_forward_few", "moe_adapter_workspace_size",
                      "moe_adapter_backward_workspace_size", "moe_adapter_forward", "moe_adapter_backward",
-                     "moe_adapter_check"):
+                     "moe_adapter_check", "moe_dropout_forward", "moe_dropout_backward"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -600,3 +618,33 @@ def moe_adapter_check(ap, ws, stream=None) -> int:
     met an id out of range, MOE_ERR_TIMEOUT, or MOE_OK."""
     with _on_device_of(ws):
         return lib().moe_adapter_check(ctypes.byref(ap), _ptr(ws), _stream(stream))
+
+
+def _dropout_types(dp, wide, narrow, step):
+    import torch
+    dt = torch.bfloat16 if dp.dtype == MOE_BF16 else torch.float32
+    for what, t in narrow:
+        if t is not None:
+            _typed(what, t, dt, (dp.N, dp.d))
+    _typed(*wide, torch.float32, (dp.N, dp.d))
+    if step is not None and (step.dtype not in (torch.int64, torch.uint64) or step.numel() != 1):
+        raise ValueError("step: expected one 64-bit integer")
+
+
+def moe_dropout_forward(dp, Y, residual, out, step=None, stream=None):
+    """out = residual + dropout(Y) (see moe_dropout_forward in include/moe.h);
+    residual may be None; step: a device tensor of one int64 that is added to
+    the offset when the kernel runs."""
+    _dropout_types(dp, ("Y", Y), (("residual", residual), ("out", out)), step)
+    with _on_device_of(Y, residual, out, step):
+        _check(lib().moe_dropout_forward(ctypes.byref(dp), _ptr(Y), _ptr(residual), _ptr(out), _ptr(step),
+                                         _stream(stream)), "moe_dropout_forward")
+
+
+def moe_dropout_backward(dp, dout, dY, step=None, stream=None):
+    """dY = the gradient of the layer's output for the gradient dout of
+    moe_dropout_forward's out, under the same params and step."""
+    _dropout_types(dp, ("dY", dY), (("dout", dout),), step)
+    with _on_device_of(dout, dY, step):
+        _check(lib().moe_dropout_backward(ctypes.byref(dp), _ptr(dout), _ptr(dY), _ptr(step), _stream(stream)),
+               "moe_dropout_backward")
