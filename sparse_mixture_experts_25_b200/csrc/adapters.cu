@@ -24,7 +24,10 @@
 // beside 16-bit adapters and three (24 bits) in fp32, where the products of
 // parts up to 2^-16 of the first are kept.  (tcgen05 tiles of 64 or 128 rows
 // would be mostly padding at these ranks: the tensor pipe is not what bounds.)
-// u and v are stored as such parts, in the sorted order.
+// u and v are stored as such parts, in the sorted order.  The tensor pipe
+// truncates its running sums: left to run over K = 1000 in fp32, y was off by
+// 4.9e-6 of its norm.  So a long sum is kept outside: the products of one stage
+// are summed from zero (small parts first) and added to it with rounding.
 //
 // A few tokens (N <= 32) take another form: no sort, one CTA per token and
 // slice of K, then one thread per output; two launches instead of three, and no
@@ -45,10 +48,11 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 64;          // rows of a tile
-constexpr int kShrinkK = 64;       // K elements staged at a time
-constexpr int kExpandCols = 128;   // columns staged at a time
+constexpr int kShrinkK = 64;       // K elements of a shrink stage
+constexpr int kStages = 4;         // stages of the shrink's and the grad's rings
 constexpr int kGradCols = 128;     // columns of a grad CTA
-constexpr int kGradRows = 32;      // tokens staged at a time
+constexpr int kGradRows = 32;      // tokens of a grad stage
+constexpr int kGradFlush = 4;      // grad stages between additions to the sums
 constexpr int kFewN = 32;          // batches of the few-token form
 constexpr int kMaxSlices = 8;      // K slices of a shrink (CTAs of a cluster)
 constexpr int kMaxSplits = 8;      // token splits of a grad
@@ -125,10 +129,7 @@ __device__ __forceinline__ void load8_parts(const __nv_bfloat16* p, bool in, uin
     out[0] = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
 }
 template <int P>
-__device__ __forceinline__ void load8_parts(const float* p, bool in, uint4 (&out)[P]) {
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 lo = in ? *reinterpret_cast<const float4*>(p) : zero;
-    const float4 hi = in ? *reinterpret_cast<const float4*>(p + 4) : zero;
+__device__ __forceinline__ void split8(float4 lo, float4 hi, uint4 (&out)[P]) {
     uint32_t a[P], b[P], c[P], d[P];
     split2<P>(lo.x, lo.y, a);
     split2<P>(lo.z, lo.w, b);
@@ -137,6 +138,22 @@ __device__ __forceinline__ void load8_parts(const float* p, bool in, uint4 (&out
 #pragma unroll
     for (int i = 0; i < P; ++i) out[i] = make_uint4(a[i], b[i], c[i], d[i]);
 }
+template <int P>
+__device__ __forceinline__ void load8_parts(const float* p, bool in, uint4 (&out)[P]) {
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    split8<P>(in ? *reinterpret_cast<const float4*>(p) : zero, in ? *reinterpret_cast<const float4*>(p + 4) : zero, out);
+}
+
+// 16 bytes global -> shared, asynchronously; zeros where !in
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 // whether the product of parts i and j counts beside operands of PA and PB parts
 template <int PA, int PB>
@@ -162,17 +179,29 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t* ids, 
     const int chunk = ((N + 31) / 32 + 31) / 32 * 32;
     const int t0 = warp * chunk, t1 = min(N, t0 + chunk);
     bool bad = false;
-    auto bucket = [&](int t) {
-        if (t >= t1) return -1;
-        const int id = ids[t];
-        if (id < -1 || id >= n_adapters) bad = true;
-        return id < 0 || id >= n_adapters ? n_adapters : id;
+    // buckets of 8 x 32 tokens from b on, loaded together
+    auto buckets = [&](int b, int (&id)[8]) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int t = b + q * 32 + lane;
+            id[q] = t < t1 ? ids[t] : -2;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const bool in = b + q * 32 + lane < t1;
+            if (in && (id[q] < -1 || id[q] >= n_adapters)) bad = true;
+            id[q] = !in ? -1 : (id[q] < 0 || id[q] >= n_adapters ? n_adapters : id[q]);
+        }
     };
-    for (int b = t0; b < t1; b += 32) {
-        const int id = bucket(b + lane);
-        const unsigned same = __match_any_sync(0xffffffffu, id);
-        if (id >= 0 && lane == __ffs(same) - 1) cnt[warp * nb + id] += __popc(same);
-        __syncwarp();
+    for (int b = t0; b < t1; b += 256) {
+        int id[8];
+        buckets(b, id);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const unsigned same = __match_any_sync(0xffffffffu, id[q]);
+            if (id[q] >= 0 && lane == __ffs(same) - 1) cnt[warp * nb + id[q]] += __popc(same);
+            __syncwarp();
+        }
     }
     if (bad) atomicOr(p.counters + CNT_DEVICE_ERROR, (unsigned long long)DEVERR_BOUNDS);
     __syncthreads();
@@ -229,28 +258,35 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t* ids, 
         const int pos = first[lo] + (i - tile0[lo]) * kRows;
         p.tiles[i] = {lo, pos, min(kRows, first[lo + 1] - pos), 0};
     }
-    for (int b = t0; b < t1; b += 32) {
-        const int t = b + lane, id = bucket(t);
-        const unsigned same = __match_any_sync(0xffffffffu, id);
-        int at = 0;
-        if (id >= 0) at = first[id] + cnt[warp * nb + id] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (id >= 0) {
-            if (lane == __ffs(same) - 1) cnt[warp * nb + id] += __popc(same);
-            p.perm[at] = t;
+    for (int b = t0; b < t1; b += 256) {
+        int id[8];
+        buckets(b, id);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const unsigned same = __match_any_sync(0xffffffffu, id[q]);
+            int at = 0;
+            if (id[q] >= 0) at = first[id[q]] + cnt[warp * nb + id[q]] + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (id[q] >= 0) {
+                if (lane == __ffs(same) - 1) cnt[warp * nb + id[q]] += __popc(same);
+                p.perm[at] = b + q * 32 + lane;
+            }
+            __syncwarp();
         }
-        __syncwarp();
     }
 }
 
 // ---------------------------------------------------------------------------
 // shrink: out[pos, q] = s_a sum_k X[tok(pos), k] M_a(q, k) as parts.
 //   NN = false: M_a is A_a [r, K] (x -> u);  NN = true: M_a is B_a [K, r] (dy -> v)
-// A CTA has one tile and one of the cluster's K slices; each warp 16 of the
-// rows.  X goes from global memory to the MMA's A registers: a lane reads 8
-// consecutive K elements of two rows and feeds them to two MMAs, the adapter's
-// elements in the same order of K.  The cluster's CTAs add their sums in slice
-// order through distributed shared memory.
+// A CTA has one tile and one of the cluster's K slices.  Stages of 64 K come
+// through a ring of asynchronous copies (the rows are gathered there).  With
+// ranks up to 64 a warp has 32 rows and one of a stage's two steps of 32 K, so
+// each adapter element read from shared memory meets 32 rows; above, 16 rows
+// and both steps.  A lane reads 8 consecutive K elements of a row and feeds
+// them to two MMAs, the adapter's elements in the same order of K.  The
+// cluster's CTAs add their sums in slice order through distributed shared
+// memory.
 // ---------------------------------------------------------------------------
 struct ShrinkArgs {
     const void* X;
@@ -262,98 +298,152 @@ struct ShrinkArgs {
     Plan p;
 };
 
+// row pitches that keep the lanes' reads apart: 16-bit rows of 64 elements, 64
+// bytes above a multiple of 128 (a quarter-warp reads 2 rows x 64 bytes);
+// 32-bit ones, 16 above (2 rows x 4 x 16 bytes, 32 apart); an adapter's rows of
+// r ranks, 16 above
+template <typename TA>
+constexpr int shrink_x_pitch() { return sizeof(TA) == 2 ? kShrinkK * 2 + 64 : kShrinkK * 4 + 16; }
+template <typename T, bool NN>
+__host__ __device__ constexpr int shrink_m_pitch(int r) {
+    return NN ? r * (int)sizeof(T) + 16 : shrink_x_pitch<T>();
+}
+template <typename T, typename TA, bool NN>
+__host__ __device__ constexpr int shrink_stage(int r) {
+    return kRows * shrink_x_pitch<TA>() + (NN ? kShrinkK : r) * shrink_m_pitch<T, NN>(r);
+}
+
 template <typename T, typename TA, bool NN, int NQ>
 __global__ void __launch_bounds__(128) adapter_shrink_kernel(const __grid_constant__ ShrinkArgs a) {
     constexpr int PA = act_parts<TA, T>(), PB = Parts<T>::self, PF = Parts<T>::f32;
+    constexpr int MR = NQ <= 8 ? 2 : 1;   // 16-row tiles of a warp
+    constexpr int STEPS = MR == 2 ? 1 : 2;
+    constexpr int kXPitch = shrink_x_pitch<TA>();
     extern __shared__ __align__(128) uint8_t smem[];
     const cg::cluster_group cluster = cg::this_cluster();
     if ((int)blockIdx.x >= *a.p.n_tiles) return;  // the same for the whole cluster
     const Tile tile = a.p.tiles[blockIdx.x];
     if (tile.adapter >= a.n_adapters) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int r = a.r;
-    // NN: [64 k][r] rows in the order that ldmatrix wants; else [r][64 k]
-    const int pitch = NN ? r * 2 + 16 : kShrinkK * 2 + 64;
-    const int part_bytes = (NN ? kShrinkK : r) * pitch;
+    const int r = a.r, m_pitch = shrink_m_pitch<T, NN>(r), stage_bytes = shrink_stage<T, TA, NN>(r);
     const TA* X = static_cast<const TA*>(a.X);
     const T* M = static_cast<const T*>(a.M) + (int64_t)tile.adapter * r * a.K;
-    const TA* row[2];
-    bool have[2];
+    // this thread's copies of a stage: 16-byte piece xp of rows xr, xr + XS, ...
+    constexpr int XPIECES = kShrinkK * (int)sizeof(TA) / 16, XS = 128 / XPIECES;
+    const int xp = tid % XPIECES, xr = tid / XPIECES;
+    const TA* row[kRows / XS];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int q = warp * 16 + g + 8 * i;
-        have[i] = q < tile.rows;
-        row[i] = X + (int64_t)(have[i] ? a.p.perm[tile.pos + q] : 0) * a.K;
+    for (int i = 0; i < kRows / XS; ++i) {
+        const int q = xr + i * XS;
+        row[i] = q < tile.rows ? X + (int64_t)a.p.perm[tile.pos + q] * a.K : nullptr;
     }
-    float acc[NQ][4] = {};
-    const int k_end = min(a.K, (int)(blockIdx.y + 1) * a.slice);
-    for (int kb = blockIdx.y * a.slice; kb < k_end; kb += kShrinkK) {
-        uint4 x[2][2][PA];
+    const int k_beg = blockIdx.y * a.slice, k_end = min(a.K, k_beg + a.slice);
+    const int chunks = k_beg < k_end ? (k_end - k_beg + kShrinkK - 1) / kShrinkK : 0;
+    auto fill = [&](int c) {
+        if (c < chunks) {
+            const uint32_t xs = smem_addr(smem) + c % kStages * stage_bytes, ms = xs + kRows * kXPitch;
+            const int kb = k_beg + c * kShrinkK;
+            const int k = kb + xp * (16 / (int)sizeof(TA));
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int k = kb + s * 32 + t * 8;
-                load8_parts<PA>(row[i] + k, have[i] && k < k_end, x[s][i]);
+            for (int i = 0; i < kRows / XS; ++i) {
+                const bool in = row[i] && k < k_end;
+                copy16(xs + (xr + i * XS) * kXPitch + xp * 16, in ? row[i] + k : X, in);
             }
-        __syncthreads();
-        for (int i = tid; i < r * (kShrinkK / 8); i += 128) {
-            uint4 v[PB];
-            int at;
-            if (NN) {
-                const int k = i / (r / 8), q = i % (r / 8) * 8;
-                load8_parts<PB>(M + (int64_t)(kb + k) * r + q, kb + k < k_end, v);
-                at = ((k & 32) + (k & 7) * 4 + (k >> 3 & 3)) * pitch + q * 2;
-            } else {
-                const int q = i / (kShrinkK / 8), k = i % (kShrinkK / 8) * 8;
-                load8_parts<PB>(M + (int64_t)q * a.K + kb + k, kb + k < k_end, v);
-                at = q * pitch + k * 2;
-            }
-#pragma unroll
-            for (int j = 0; j < PB; ++j) *reinterpret_cast<uint4*>(smem + j * part_bytes + at) = v[j];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                if (n * 8 >= r) break;
-#pragma unroll
-                for (int j = 0; j < PB; ++j) {
-                    uint32_t b[4];
-                    if (NN) {
-                        const int m = lane >> 3, i = lane & 7;
-                        ldmatrix_x4_trans(b, smem + j * part_bytes +
-                                                 (s * 32 + ((i & 1) + 2 * m) * 4 + (i >> 1)) * pitch + n * 16);
-                    } else {
-                        const uint4 v = *reinterpret_cast<const uint4*>(smem + j * part_bytes + (n * 8 + g) * pitch +
-                                                                        (s * 32 + t * 8) * 2);
-                        b[0] = v.x;
-                        b[1] = v.y;
-                        b[2] = v.z;
-                        b[3] = v.w;
-                    }
-#pragma unroll
-                    for (int i = 0; i < PA; ++i) {
-                        if (!counts<PA, PB>(i, j)) continue;
-                        const uint4 &lo = x[s][0][i], &hi = x[s][1][i];
-                        mma_bf16(acc[n], lo.x, hi.x, lo.y, hi.y, b[0], b[1]);
-                        mma_bf16(acc[n], lo.z, hi.z, lo.w, hi.w, b[2], b[3]);
-                    }
+            constexpr int E = 16 / (int)sizeof(T);  // elements of a piece
+            const int per = NN ? r / E : kShrinkK / E;
+            for (int i = tid; i < (NN ? kShrinkK : r) * per; i += 128) {
+                const int major = i / per, minor = i % per * E;
+                if (NN) {
+                    // K rows in the order that puts the four lanes' rows next to one another
+                    const int at = (major & 32) + (major & 7) * 4 + (major >> 3 & 3);
+                    const bool in = kb + major < k_end;
+                    copy16(ms + at * m_pitch + minor * (int)sizeof(T), in ? M + (int64_t)(kb + major) * r + minor : M, in);
+                } else {
+                    const bool in = kb + minor < k_end;
+                    copy16(ms + major * m_pitch + minor * (int)sizeof(T), in ? M + (int64_t)major * a.K + kb + minor : M, in);
                 }
             }
         }
-    }
-    // the cluster's sums, slice by slice, then the parts
-    __syncthreads();
-    float* mine = reinterpret_cast<float*>(smem);  // [64][r]
+        copies_commit();
+    };
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        if (n * 8 >= r) break;
-        const int at = (warp * 16 + g) * r + n * 8 + 2 * t;
-        *reinterpret_cast<float2*>(mine + at) = make_float2(acc[n][0], acc[n][1]);
-        *reinterpret_cast<float2*>(mine + at + 8 * r) = make_float2(acc[n][2], acc[n][3]);
+    for (int c = 0; c < kStages - 1; ++c) fill(c);
+    const int row0 = MR == 2 ? (warp & 1) * 32 : warp * 16;
+    float sum[MR][NQ][4] = {};
+    for (int c = 0; c < chunks; ++c) {
+        copies_wait<kStages - 2>();
+        __syncthreads();
+        fill(c + kStages - 1);
+        const uint8_t* xs = smem + c % kStages * stage_bytes;
+        const uint8_t* ms = xs + kRows * kXPitch;
+        uint4 x[STEPS][MR][2][PA];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int m = 0; m < MR; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    load8_parts<PA>(reinterpret_cast<const TA*>(xs + (row0 + m * 16 + g + 8 * i) * kXPitch) +
+                                        (MR == 2 ? warp >> 1 : s) * 32 + t * 8,
+                                    true, x[s][m][i]);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            if (n * 8 >= r) break;
+            uint4 b[STEPS][PB];
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int step = MR == 2 ? warp >> 1 : s;
+                if constexpr (!NN) {
+                    load8_parts<PB>(reinterpret_cast<const T*>(ms + (n * 8 + g) * m_pitch) + step * 32 + t * 8, true, b[s]);
+                } else if constexpr (sizeof(T) == 2) {
+                    const int m = lane >> 3, i = lane & 7;
+                    uint32_t v[4];
+                    ldmatrix_x4_trans(v, ms + (step * 32 + ((i & 1) + 2 * m) * 4 + (i >> 1)) * m_pitch + n * 16);
+                    b[s][0] = make_uint4(v[0], v[1], v[2], v[3]);
+                } else {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = *reinterpret_cast<const float*>(ms + (step * 32 + e * 4 + t) * m_pitch + (n * 8 + g) * 4);
+                    split8<PB>(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), b[s]);
+                }
+            }
+            float acc[MR][4] = {};
+            // small products first
+#pragma unroll
+            for (int level = (PA > PB ? PA : PB) - 1; level >= 0; --level)
+#pragma unroll
+                for (int j = 0; j < PB; ++j) {
+                    const int i = level - j;
+                    if (i < 0 || i >= PA) continue;
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                        for (int m = 0; m < MR; ++m) {
+                            const uint4 &lo = x[s][m][0][i], &hi = x[s][m][1][i];
+                            mma_bf16(acc[m], lo.x, hi.x, lo.y, hi.y, b[s][j].x, b[s][j].y);
+                            mma_bf16(acc[m], lo.z, hi.z, lo.w, hi.w, b[s][j].z, b[s][j].w);
+                        }
+                }
+#pragma unroll
+            for (int m = 0; m < MR; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[m][n][e] += acc[m][e];
+        }
     }
+    // the cluster's sums, slice by slice (and step by step), then the parts
+    copies_wait<0>();
+    __syncthreads();
+    float* mine = reinterpret_cast<float*>(smem);  // [MR][64][r]
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            if (n * 8 >= r) break;
+            const int at = ((MR == 2 ? warp >> 1 : 0) * kRows + row0 + m * 16 + g) * r + n * 8 + 2 * t;
+            *reinterpret_cast<float2*>(mine + at) = make_float2(sum[m][n][0], sum[m][n][1]);
+            *reinterpret_cast<float2*>(mine + at + 8 * r) = make_float2(sum[m][n][2], sum[m][n][3]);
+        }
     cluster.sync();
     const int slices = cluster.num_blocks(), rank = cluster.block_rank();
     const float scale = a.scale[tile.adapter];
@@ -361,9 +451,13 @@ __global__ void __launch_bounds__(128) adapter_shrink_kernel(const __grid_consta
     for (int i = rank * 128 + tid; i < pairs; i += 128 * slices) {
         float2 s = make_float2(0.f, 0.f);
         for (int q = 0; q < slices; ++q) {
-            const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(mine, q) + 2 * i);
-            s.x += v.x;
-            s.y += v.y;
+            const float* theirs = cluster.map_shared_rank(mine, q) + 2 * i;
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                const float2 v = *reinterpret_cast<const float2*>(theirs + m * kRows * r);
+                s.x += v.x;
+                s.y += v.y;
+            }
         }
         uint32_t out[PF];
         split2<PF>(s.x * scale, s.y * scale, out);
@@ -378,7 +472,10 @@ __global__ void __launch_bounds__(128) adapter_shrink_kernel(const __grid_consta
 // expand: out[tok(pos), j] = base[tok, j] (+ out[tok, j]) + sum_q in[pos, q] M_a(q, j)
 //   NN = false: M_a is B_a [J, r] (u -> y);  NN = true: M_a is A_a [r, J] (v -> dx)
 // A CTA has one tile and a span of columns; each warp 16 of the rows, their
-// parts of u in registers throughout.
+// parts of u in registers throughout, the span's part of the adapter in shared
+// memory.  Per 32 columns a lane has 8 consecutive ones of two rows (the four
+// MMA tiles take the columns in that order), so a row is read and written in
+// whole lines; what is added to is fetched one step ahead.
 // ---------------------------------------------------------------------------
 struct ExpandArgs {
     const __nv_bfloat16* in;  // [parts][N][r]
@@ -395,12 +492,17 @@ struct ExpandArgs {
 // 32 bytes) do not collide: 32 above a multiple of 64
 __host__ __device__ constexpr int expand_pitch(int r) { return (2 * r + 31) / 64 * 64 + 32; }
 
+// shared memory of a span of columns of an adapter
+template <typename T, bool NN, int NK>
+__host__ __device__ constexpr int expand_part(int span) {
+    return NN ? NK * 16 * (span * 2 + 16) : span * expand_pitch(NK * 16);
+}
+
 template <typename T, bool NN, int NK>
 __global__ void __launch_bounds__(128) adapter_expand_kernel(const __grid_constant__ ExpandArgs a) {
     constexpr int PB = Parts<T>::self, PF = Parts<T>::f32;
     constexpr int R = NK * 16;
-    constexpr int kPitch = NN ? kExpandCols * 2 + 16 : expand_pitch(R);
-    constexpr int kPartBytes = (NN ? R : kExpandCols) * kPitch;
+    const int pitch = NN ? a.span * 2 + 16 : expand_pitch(R), part_bytes = expand_part<T, NN, NK>(a.span);
     extern __shared__ __align__(128) uint8_t smem[];
     if ((int)blockIdx.x >= *a.p.n_tiles) return;
     const Tile tile = a.p.tiles[blockIdx.x];
@@ -410,14 +512,45 @@ __global__ void __launch_bounds__(128) adapter_expand_kernel(const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int r = a.r, J = a.J;
     const T* M = static_cast<const T*>(a.M) + (none ? 0 : (int64_t)tile.adapter * r * J);
-    int64_t tok[2];
+    const int jb = blockIdx.y * a.span, cols = min(a.span, J - jb);
+    // place of column j among the span's: the four tiles of 32 columns take pairs in turn
+    auto place = [](int j) { return (j & ~31) + (j >> 1 & 3) * 8 + (j >> 3 & 3) * 2 + (j & 1); };
+    if (!none) {
+        const int groups = (cols + 31) / 32 * 32;
+        if (NN) {
+            for (int i = tid; i < R * (groups / 8); i += 128) {
+                const int k = i / (groups / 8), j = i % (groups / 8) * 8;
+                uint4 v[PB];
+                load8_parts<PB>(M + (int64_t)k * J + jb + j, k < r && j < cols, v);
+                // K rows in the order that puts the four lanes' rows next to one another
+                uint8_t* at = smem + ((k & ~15) + (k & 3) * 4 + (k >> 2 & 3)) * pitch + place(j) * 2;
+#pragma unroll
+                for (int q = 0; q < PB; ++q) {
+                    *reinterpret_cast<uint32_t*>(at + q * part_bytes) = v[q].x;
+                    *reinterpret_cast<uint32_t*>(at + q * part_bytes + 16) = v[q].y;
+                    *reinterpret_cast<uint32_t*>(at + q * part_bytes + 32) = v[q].z;
+                    *reinterpret_cast<uint32_t*>(at + q * part_bytes + 48) = v[q].w;
+                }
+            }
+        } else {
+            for (int i = tid; i < groups * (R / 8); i += 128) {
+                const int j = i / (R / 8), k = i % (R / 8) * 8;
+                uint4 v[PB];
+                load8_parts<PB>(M + (int64_t)(jb + j) * r + k, k < r && j < cols, v);
+#pragma unroll
+                for (int q = 0; q < PB; ++q)
+                    *reinterpret_cast<uint4*>(smem + q * part_bytes + place(j) * pitch + k * 2) = v[q];
+            }
+        }
+    }
+    int64_t at[2];
     bool have[2];
     uint32_t u[PF][NK][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int q = warp * 16 + g + 8 * i;
         have[i] = q < tile.rows;
-        tok[i] = have[i] ? a.p.perm[tile.pos + q] : 0;
+        at[i] = (have[i] ? (int64_t)a.p.perm[tile.pos + q] : 0) * J + jb + 8 * t;
 #pragma unroll
         for (int j = 0; j < PF; ++j)
 #pragma unroll
@@ -431,69 +564,56 @@ __global__ void __launch_bounds__(128) adapter_expand_kernel(const __grid_consta
                 u[j][s][2 + i] = v.y;
             }
     }
-    const int j_end = min(J, (int)(blockIdx.y + 1) * a.span);
-    for (int jb = blockIdx.y * a.span; jb < j_end; jb += kExpandCols) {
-        const int cols = min(kExpandCols, j_end - jb);
-        if (!none) {
-            __syncthreads();
-            if (NN) {
-                for (int i = tid; i < R * (kExpandCols / 8); i += 128) {
-                    const int k = i / (kExpandCols / 8), j = i % (kExpandCols / 8) * 8;
-                    uint4 v[PB];
-                    load8_parts<PB>(M + (int64_t)k * J + jb + j, k < r && j < cols, v);
-                    const int at = ((k & ~15) + (k & 3) * 4 + (k >> 2 & 3)) * kPitch + j * 2;
+    // what 32 columns from n0 on are added to: 8 of two rows
+    auto fetch = [&](int n0, float4 (&v)[2][2]) {
 #pragma unroll
-                    for (int q = 0; q < PB; ++q) *reinterpret_cast<uint4*>(smem + q * kPartBytes + at) = v[q];
-                }
-            } else {
-                for (int i = tid; i < kExpandCols * (R / 8); i += 128) {
-                    const int j = i / (R / 8), k = i % (R / 8) * 8;
-                    uint4 v[PB];
-                    load8_parts<PB>(M + (int64_t)(jb + j) * r + k, k < r && j < cols, v);
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int q = 0; q < PB; ++q)
-                        *reinterpret_cast<uint4*>(smem + q * kPartBytes + j * kPitch + k * 2) = v[q];
+            for (int h = 0; h < 2; ++h) {
+                v[i][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!have[i] || n0 + 8 * t >= cols) continue;
+                if (a.base) v[i][h] = *reinterpret_cast<const float4*>(a.base + at[i] + n0 + 4 * h);
+                if (a.add_out) {
+                    const float4 w = *reinterpret_cast<const float4*>(a.out + at[i] + n0 + 4 * h);
+                    v[i][h].x += w.x;
+                    v[i][h].y += w.y;
+                    v[i][h].z += w.z;
+                    v[i][h].w += w.w;
                 }
             }
-            __syncthreads();
-        }
+    };
+    float4 next[2][2];
+    fetch(0, next);
+    __syncthreads();
 #pragma unroll 1
-        for (int n0 = 0; n0 < cols; n0 += 32) {
-            // four column tiles: what is added to, then the products, then the stores
-            float2 add[4][2];
+    for (int n0 = 0; n0 < cols; n0 += 32) {
+        float4 add[2][2];
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = n0 + n * 8 + 2 * t;
-                    const bool in = have[i] && j < cols;
-                    const int64_t at = tok[i] * J + jb + j;
-                    float2 v = make_float2(0.f, 0.f);
-                    if (in && a.base) v = *reinterpret_cast<const float2*>(a.base + at);
-                    if (in && a.add_out) {
-                        const float2 w = *reinterpret_cast<const float2*>(a.out + at);
-                        v.x += w.x;
-                        v.y += w.y;
-                    }
-                    add[n][i] = v;
-                }
-            float acc[4][4] = {};
-            if (!none) {
+            for (int h = 0; h < 2; ++h) add[i][h] = next[i][h];
+        if (n0 + 32 < cols) fetch(n0 + 32, next);
+        float acc[4][4] = {};
+        if (!none) {
 #pragma unroll
-                for (int s = 0; s < NK; ++s) {
+            for (int level = (PF > PB ? PF : PB) - 1; level >= 0; --level)  // small products first
 #pragma unroll
-                    for (int q = 0; q < PB; ++q) {
+                for (int q = 0; q < PB; ++q) {
+                    const int j = level - q;
+                    if (j < 0 || j >= PF) continue;
+#pragma unroll
+                    for (int s = 0; s < NK; ++s) {
                         uint32_t b[4][2];
                         if (NN) {
                             // two column tiles at a time: (b0, b1) of each
                             const int m = lane >> 3, i = lane & 7;
-                            const uint8_t* at = smem + q * kPartBytes +
-                                                (s * 16 + ((i & 1) + 2 * (m & 1)) * 4 + (i >> 1)) * kPitch +
-                                                (n0 + (m >> 1) * 8) * 2;
+                            const uint8_t* p = smem + q * part_bytes +
+                                               (s * 16 + ((i & 1) + 2 * (m & 1)) * 4 + (i >> 1)) * pitch +
+                                               (n0 + (m >> 1) * 8) * 2;
                             uint32_t v[4];
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                ldmatrix_x4_trans(v, at + h * 32);
+                                ldmatrix_x4_trans(v, p + h * 32);
                                 b[2 * h][0] = v[0];
                                 b[2 * h][1] = v[1];
                                 b[2 * h + 1][0] = v[2];
@@ -503,30 +623,28 @@ __global__ void __launch_bounds__(128) adapter_expand_kernel(const __grid_consta
 #pragma unroll
                             for (int n = 0; n < 4; ++n) {
                                 const uint2 v = *reinterpret_cast<const uint2*>(
-                                    smem + q * kPartBytes + (n0 + n * 8 + g) * kPitch + (s * 16 + 4 * t) * 2);
+                                    smem + q * part_bytes + (n0 + n * 8 + g) * pitch + (s * 16 + 4 * t) * 2);
                                 b[n][0] = v.x;
                                 b[n][1] = v.y;
                             }
                         }
 #pragma unroll
-                        for (int j = 0; j < PF; ++j) {
-                            if (!counts<PF, PB>(j, q)) continue;
-#pragma unroll
-                            for (int n = 0; n < 4; ++n)
-                                mma_bf16(acc[n], u[j][s][0], u[j][s][1], u[j][s][2], u[j][s][3], b[n][0], b[n][1]);
-                        }
+                        for (int n = 0; n < 4; ++n)
+                            mma_bf16(acc[n], u[j][s][0], u[j][s][1], u[j][s][2], u[j][s][3], b[n][0], b[n][1]);
                     }
                 }
+        }
+        // tile n has columns 2 n, 2 n + 1 of this lane's 8
+        if (n0 + 8 * t < cols) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!have[i]) continue;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float4*>(a.out + at[i] + n0 + 4 * h) =
+                        make_float4(add[i][h].x + acc[2 * h][2 * i], add[i][h].y + acc[2 * h][2 * i + 1],
+                                    add[i][h].z + acc[2 * h + 1][2 * i], add[i][h].w + acc[2 * h + 1][2 * i + 1]);
             }
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = n0 + n * 8 + 2 * t;
-                    if (have[i] && j < cols)
-                        *reinterpret_cast<float2*>(a.out + tok[i] * J + jb + j) =
-                            make_float2(add[n][i].x + acc[n][2 * i], add[n][i].y + acc[n][2 * i + 1]);
-                }
         }
     }
 }
@@ -534,9 +652,13 @@ __global__ void __launch_bounds__(128) adapter_expand_kernel(const __grid_consta
 // ---------------------------------------------------------------------------
 // grad: G_a(q, j) = sum over adapter a's tokens of in[pos, q] Z[tok(pos), j]
 //   TRANS = false: dA_a [r, J] from v and x;  TRANS = true: dB_a [J, r] from u and dy
-// A CTA has one adapter, 128 columns and one split of the tokens; each warp 16
-// of the columns and all ranks.  Both operands have K (the tokens) as their
-// slow axis and come through shared memory by transposing loads.
+// A CTA has one adapter, 128 columns and one split of the tokens; each warp 32
+// of the columns and all ranks.  The tokens' parts of u or v, which all warps
+// need, and their places come through a ring of asynchronous copies; a row of Z
+// is used by one warp only and goes from global memory to its registers a
+// stage ahead: a lane reads 4 consecutive columns of four rows, and the four MMA
+// tiles take the columns in that order, so a lane's results are 8 consecutive
+// columns too.
 // ---------------------------------------------------------------------------
 struct GradArgs {
     const __nv_bfloat16* in;  // [parts][N][r]
@@ -547,97 +669,172 @@ struct GradArgs {
     Plan p;
 };
 
+template <int PF, int MT>
+constexpr int grad_stage() { return PF * kGradRows * (MT * 32 + 16) + kGradRows * 4; }
+template <int PF, int MT>
+constexpr size_t grad_smem() { return (size_t)kStages * grad_stage<PF, MT>() + (size_t)MT * 16 * 128 * 4; }
+
+// 4 consecutive elements as they are in memory
+template <typename TZ>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
+};
+// column n of two rows as P packed parts
+template <int P>
+__device__ __forceinline__ void pair_parts(const Raw4<float>& a, const Raw4<float>& b, int n, uint32_t (&out)[P]) {
+    split2<P>(n == 0 ? a.v.x : n == 1 ? a.v.y : n == 2 ? a.v.z : a.v.w,
+              n == 0 ? b.v.x : n == 1 ? b.v.y : n == 2 ? b.v.z : b.v.w, out);
+}
+template <int P>
+__device__ __forceinline__ void pair_parts(const Raw4<__nv_bfloat16>& a, const Raw4<__nv_bfloat16>& b, int n,
+                                           uint32_t (&out)[P]) {
+    static_assert(P == 1, "16-bit operands are one part");
+    out[0] = __byte_perm(n < 2 ? a.v.x : a.v.y, n < 2 ? b.v.x : b.v.y, n & 1 ? 0x7632 : 0x5410);
+}
+
 template <typename T, typename TZ, bool TRANS, int MT>
-__global__ void __launch_bounds__(256) adapter_grad_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(128) adapter_grad_kernel(const __grid_constant__ GradArgs a) {
     constexpr int PZ = act_parts<TZ, T>(), PF = Parts<T>::f32;
-    constexpr int kInPitch = MT * 32 + 16, kZPitch = kGradCols * 2 + 16;
-    constexpr int kInPart = kGradRows * kInPitch, kZPart = kGradRows * kZPitch;
+    constexpr int kInPitch = MT * 32 + 16, kInPart = kGradRows * kInPitch, kStage = grad_stage<PF, MT>();
+    constexpr int STEPS = kGradRows / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* in_s = smem;
-    uint8_t* z_s = smem + PF * kInPart;
+    float* sums = reinterpret_cast<float*>(smem + kStages * kStage);  // [MT * 16][128 threads]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int adapter = blockIdx.y, splits = gridDim.z, split = blockIdx.z;
-    const int r = a.r, J = a.J, jb = blockIdx.x * kGradCols;
+    const int r = a.r, J = a.J;
     const int seg0 = a.p.seg[adapter], seg1 = a.p.seg[adapter + 1];
-    const int chunks = (seg1 - seg0 + kGradRows - 1) / kGradRows;
-    const int c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
-    const TZ* Z = static_cast<const TZ*>(a.Z);
-    float acc[MT][2][4] = {};
-    // this thread's elements of a chunk: of Z, 8 columns of two rows; of in, 8 ranks of some rows
-    const int zc = tid & 15, zr = tid >> 4;
-    uint4 z[2][PZ];
-    auto load_z = [&](int c) {
+    const int all = (seg1 - seg0 + kGradRows - 1) / kGradRows;
+    const int c0 = (int)((int64_t)all * split / splits), c1 = (int)((int64_t)all * (split + 1) / splits);
+    const int col = blockIdx.x * kGradCols + warp * 32 + 4 * g;  // this lane's columns of Z
+    const TZ* Z = static_cast<const TZ*>(a.Z) + col;
+    const bool col_in = col < J;
+    auto fill = [&](int c) {
+        if (c < c1) {
+            const uint32_t st = smem_addr(smem) + (c - c0) % kStages * kStage;
+            const int pos = seg0 + c * kGradRows;
+            for (int i = tid; i < kGradRows * MT * 2; i += 128) {
+                const int row = i / (MT * 2), q = i % (MT * 2) * 8;
+                const bool in = pos + row < seg1 && q < r;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int pos = seg0 + c * kGradRows + zr + 16 * h;
-            const bool in = pos < seg1 && jb + zc * 8 < J;
-            const int64_t tok = in ? a.p.perm[pos] : 0;
-            load8_parts<PZ>(Z + tok * J + jb + zc * 8, in, z[h]);
+                for (int j = 0; j < PF; ++j)
+                    copy16(st + j * kInPart + row * kInPitch + q * 2,
+                           in ? a.in + ((int64_t)j * a.N + pos + row) * r + q : a.in, in);
+            }
+            if (tid < kGradRows)  // 4 bytes each: the places need not be 16-byte aligned
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(st + PF * kInPart + tid * 4),
+                             "l"(a.p.perm + (pos + tid < seg1 ? pos + tid : 0)), "r"(pos + tid < seg1 ? 4 : 0)
+                             : "memory");
         }
+        copies_commit();
     };
-    if (c0 < c1) load_z(c0);
-    for (int c = c0; c < c1; ++c) {
-        __syncthreads();
+    // rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of each step of 16 tokens
+    auto fetch = [&](int c, Raw4<TZ> (&z)[STEPS][4]) {
+        const int32_t* tok = reinterpret_cast<const int32_t*>(smem + (c - c0) % kStages * kStage + PF * kInPart);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-            for (int q = 0; q < PZ; ++q)
-                *reinterpret_cast<uint4*>(z_s + q * kZPart + (zr + 16 * h) * kZPitch + zc * 16) = z[h][q];
-        for (int i = tid; i < kGradRows * MT * 2; i += 256) {
-            const int row = i / (MT * 2), q = i % (MT * 2) * 8, pos = seg0 + c * kGradRows + row;
+            for (int i = 0; i < 4; ++i) {
+                const int row = s * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+                if (col_in && seg0 + c * kGradRows + row < seg1) z[s][i].load(Z + (int64_t)tok[row] * J);
+                else z[s][i].zero();
+            }
+    };
 #pragma unroll
-            for (int j = 0; j < PF; ++j) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (pos < seg1 && q < r) v = *reinterpret_cast<const uint4*>(a.in + ((int64_t)j * a.N + pos) * r + q);
-                *reinterpret_cast<uint4*>(in_s + j * kInPart + row * kInPitch + q * 2) = v;
+    for (int c = 0; c < kStages - 1; ++c) fill(c0 + c);
+    float acc[MT][4][4] = {};
+    auto flush = [&](bool first, bool last) {
+#pragma unroll
+        for (int i = 0; i < MT * 16; ++i) {
+            float& v = acc[i / 16][i / 4 % 4][i % 4];
+            if (!first) v += sums[i * 128 + tid];
+            if (!last) {
+                sums[i * 128 + tid] = v;
+                v = 0.f;
             }
         }
+    };
+    Raw4<TZ> z[STEPS][4];
+    if (c0 < c1) {
+        copies_wait<kStages - 2>();
         __syncthreads();
-        if (c + 1 < c1) load_z(c + 1);
+        fetch(c0, z);
+    }
+    bool first = true;
+    for (int c = c0; c < c1; ++c) {
+        copies_wait<kStages - 3>();  // this stage and the next
+        __syncthreads();
+        fill(c + kStages - 1);
+        Raw4<TZ> ahead[STEPS][4];
+        if (c + 1 < c1) fetch(c + 1, ahead);
+        const uint8_t* st = smem + (c - c0) % kStages * kStage;
 #pragma unroll
-        for (int s = 0; s < kGradRows / 16; ++s) {
+        for (int s = 0; s < STEPS; ++s) {
             const int m = lane >> 3, i = lane & 7;
-            // B: (k 0-7, n 0-7), (k 8-15, n 0-7), then the next column tile
-            uint32_t b[PZ][4];
+            uint32_t b[4][2][PZ];
 #pragma unroll
-            for (int q = 0; q < PZ; ++q)
-                ldmatrix_x4_trans(b[q], z_s + q * kZPart + (s * 16 + (m & 1) * 8 + i) * kZPitch +
-                                            (warp * 16 + (m >> 1) * 8) * 2);
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) pair_parts<PZ>(z[s][2 * h], z[s][2 * h + 1], n, b[n][h]);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-                for (int j = 0; j < PF; ++j) {
+                for (int j = PF - 1; j >= 0; --j) {
                     // A: (m 0-7, k 0-7), (m 8-15, k 0-7), (m 0-7, k 8-15), (m 8-15, k 8-15)
                     uint32_t v[4];
-                    ldmatrix_x4_trans(v, in_s + j * kInPart + (s * 16 + (m >> 1) * 8 + i) * kInPitch +
+                    ldmatrix_x4_trans(v, st + j * kInPart + (s * 16 + (m >> 1) * 8 + i) * kInPitch +
                                              (mt * 16 + (m & 1) * 8) * 2);
 #pragma unroll
-                    for (int q = 0; q < PZ; ++q) {
+                    for (int q = PZ - 1; q >= 0; --q) {
                         if (!counts<PF, PZ>(j, q)) continue;
-                        mma_bf16(acc[mt][0], v[0], v[1], v[2], v[3], b[q][0], b[q][1]);
-                        mma_bf16(acc[mt][1], v[0], v[1], v[2], v[3], b[q][2], b[q][3]);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+                            mma_bf16(acc[mt][n], v[0], v[1], v[2], v[3], b[n][0][q], b[n][1][q]);
                     }
                 }
             }
         }
+        if ((c - c0) % kGradFlush == kGradFlush - 1 && c + 1 < c1) {
+            flush(first, false);
+            first = false;
+        }
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[s][i] = ahead[s][i];
     }
+    flush(first, true);
+    copies_wait<0>();
+    // tile n has columns 8 t + n and 8 t + 4 + n of the warp's 32
     float* out = a.out + ((int64_t)split * a.n_adapters + adapter) * r * J;
+    const int j = blockIdx.x * kGradCols + warp * 32 + 8 * t;
+    if (j >= J) return;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int h = 0; h < 2; ++h) {
+            const int q = mt * 16 + g + 8 * h;
+            if (q >= r) continue;
+            if (TRANS) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int q = mt * 16 + g + 8 * h, j = jb + warp * 16 + n * 8 + 2 * t;
-                if (q >= r || j >= J) continue;
-                const float v0 = acc[mt][n][2 * h], v1 = acc[mt][n][2 * h + 1];
-                if (TRANS) {
-                    out[(int64_t)j * r + q] = v0;
-                    out[(int64_t)(j + 1) * r + q] = v1;
-                } else {
-                    *reinterpret_cast<float2*>(out + (int64_t)q * J + j) = make_float2(v0, v1);
-                }
+                for (int e = 0; e < 8; ++e) out[(int64_t)(j + e) * r + q] = acc[mt][e & 3][2 * h + (e >> 2)];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *reinterpret_cast<float4*>(out + (int64_t)q * J + j + 4 * e) =
+                        make_float4(acc[mt][0][2 * h + e], acc[mt][1][2 * h + e], acc[mt][2][2 * h + e],
+                                    acc[mt][3][2 * h + e]);
             }
+        }
 }
 
 __global__ void __launch_bounds__(256) adapter_reduce_kernel(const float4* part, int splits, int64_t n4, float4* out) {
@@ -781,12 +978,12 @@ int64_t tile_bound(const moe_adapter_params& p) {
     return p.N / kRows + std::min<int64_t>(p.n_adapters + 1, p.N);
 }
 
-// K slices of a shrink: enough CTAs for two waves of the likely tiles, at least 512 of K each
+// K slices of a shrink: enough CTAs for two waves of the likely tiles, at least two stages of K each
 int shrink_slices(const moe_adapter_params& p, int K) {
     const int64_t tiles = p.N / kRows + (std::min<int64_t>(p.n_adapters, p.N) + 1) / 2;
     const int64_t want = (4 * (int64_t)num_sms() + tiles - 1) / std::max<int64_t>(tiles, 1);
     int s = 1;
-    while (s * 2 <= kMaxSlices && s * 2 <= want && K / (s * 2) >= 512) s *= 2;
+    while (s * 2 <= kMaxSlices && s * 2 <= want && K / (s * 2) >= 2 * kShrinkK) s *= 2;
     return s;
 }
 
@@ -797,7 +994,7 @@ int few_slices(int64_t N, int K) {
 // token splits of a grad, whose partial sums a reduction adds in order
 int grad_splits(const moe_adapter_params& p, int J) {
     const int64_t ctas = (int64_t)((J + kGradCols - 1) / kGradCols) * p.n_adapters;
-    const int64_t want = (2 * (int64_t)num_sms() + ctas - 1) / ctas;
+    const int64_t want = (4 * (int64_t)num_sms() + ctas - 1) / ctas;
     return (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, want, p.N / 256}));
 }
 
@@ -860,10 +1057,9 @@ cudaError_t launch_shrink_q(const moe_adapter_params& p, ShrinkArgs a, cudaStrea
     constexpr auto kern = adapter_shrink_kernel<T, TA, NN, NQ>;
     const int slices = shrink_slices(p, a.K);
     a.slice = ((a.K + slices - 1) / slices + kShrinkK - 1) / kShrinkK * kShrinkK;
-    const size_t staged = (size_t)Parts<T>::self * (NN ? (size_t)kShrinkK * (p.r * 2 + 16) : (size_t)p.r * (kShrinkK * 2 + 64));
-    const size_t smem = std::max(staged, (size_t)kRows * p.r * 4);
-    constexpr size_t most = std::max((size_t)Parts<T>::self * (NN ? kShrinkK * (NQ * 16 + 16) : NQ * 8 * (kShrinkK * 2 + 64)),
-                                     (size_t)kRows * NQ * 8 * 4);
+    const size_t smem = std::max((size_t)kStages * shrink_stage<T, TA, NN>(p.r), (size_t)2 * kRows * p.r * 4);
+    constexpr size_t most = std::max((size_t)kStages * shrink_stage<T, TA, NN>(NQ * 8), (size_t)2 * kRows * NQ * 8 * 4);
+    static_assert(most <= 232448, "shared memory per CTA");
     cudaError_t e = allow_smem_once<kern>(most);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -904,16 +1100,17 @@ cudaError_t launch_shrink(const moe_adapter_params& p, const TA* X, const T* M, 
 template <typename T, bool NN, int NK>
 cudaError_t launch_expand_k(const moe_adapter_params& p, ExpandArgs a, cudaStream_t st) {
     constexpr auto kern = adapter_expand_kernel<T, NN, NK>;
-    constexpr size_t smem = (size_t)Parts<T>::self * (NN ? NK * 16 * (kExpandCols * 2 + 16) : kExpandCols * expand_pitch(NK * 16));
-    static_assert(smem <= 232448, "shared memory per CTA");
-    cudaError_t e = allow_smem_once<kern>(smem);
-    if (e != cudaSuccess) return e;
-    // columns of a CTA: as many as leave two waves of CTAs
+    // columns of a CTA: at most what leaves room for two CTAs on an SM, and few
+    // enough that there are CTAs for two waves
     const int64_t tiles = p.N / kRows + 1;
-    a.span = 4 * kExpandCols;
-    while (a.span > kExpandCols && tiles * ((a.J + a.span - 1) / a.span) < 2 * num_sms()) a.span /= 2;
+    auto smem = [](int span) { return (size_t)Parts<T>::self * expand_part<T, NN, NK>(span); };
+    static_assert((size_t)Parts<T>::self * expand_part<T, NN, NK>(128) <= 232448, "shared memory per CTA");
+    a.span = 512;
+    while (a.span > 128 && (smem(a.span) > 100 * 1024 || tiles * ((a.J + a.span - 1) / a.span) < 2 * num_sms())) a.span /= 2;
+    cudaError_t e = allow_smem_once<kern>(std::max(smem(128), (size_t)100 * 1024));
+    if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)tile_bound(p), (unsigned)((a.J + a.span - 1) / a.span), 1);
-    kern<<<grid, 128, smem, st>>>(a);
+    kern<<<grid, 128, smem(a.span), st>>>(a);
     return cudaGetLastError();
 }
 
@@ -940,10 +1137,11 @@ cudaError_t launch_expand(const moe_adapter_params& p, const __nv_bfloat16* in, 
 template <typename T, typename TZ, bool TRANS, int MT>
 cudaError_t launch_grad_m(const GradArgs& a, dim3 grid, cudaStream_t st) {
     constexpr auto kern = adapter_grad_kernel<T, TZ, TRANS, MT>;
-    constexpr size_t smem = (size_t)kGradRows * (Parts<T>::f32 * (MT * 32 + 16) + act_parts<TZ, T>() * (kGradCols * 2 + 16));
+    constexpr size_t smem = grad_smem<Parts<T>::f32, MT>();
+    static_assert(smem <= 232448, "shared memory per CTA");
     cudaError_t e = allow_smem_once<kern>(smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, 256, smem, st>>>(a);
+    kern<<<grid, 128, smem, st>>>(a);
     return cudaGetLastError();
 }
 

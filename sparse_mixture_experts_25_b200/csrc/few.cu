@@ -652,11 +652,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         const uint4 zero4 = make_uint4(0, 0, 0, 0);
         // bf16: one group's 16 weight rows against its R token rows (`planes`
         // parts each), summed over K: the warps take the steps of 32 in turn
+        // (The tensor pipe truncates its running sums, so a piece's products are
+        // summed from zero and added to the sum outside, with rounding: left to
+        // run over K, Y was off by 2.5e-6 of its norm, ten times as much.)
         auto mma_rows = [&](auto tiles, int K, int piece, int pitch, int R, auto planes,
-                            float (&acc)[4][decltype(tiles)::value][4]) {
+                            float (&sum)[decltype(tiles)::value][4]) {
             constexpr int M = decltype(tiles)::value;  // column tiles of 8
             for (int kb = 0; kb < K; kb += piece) {
                 const int len = min(piece, K - kb);
+                float acc[4][M][4] = {};
                 const uint8_t* st = ring + pos.stage * SB;
                 if (warp_wait_bounded(&full[pos.stage], pos.phase, abort_flag, a.counters)) {
 #pragma unroll 4
@@ -681,6 +685,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[pos.stage]);
                 pos.next(ST);
+#pragma unroll
+                for (int n = 0; n < M; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        sum[n][i] += acc[0][n][i] + acc[1][n][i];
+                        if (decltype(planes)::value > 1) sum[n][i] += acc[2][n][i] + acc[3][n][i];
+                    }
             }
         };
         // fp32: weight rows `warp` and `warp + 8` of the stage against R token rows
@@ -730,15 +741,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                 float* mine = red + ((tile & 1) * 8 + warp) * (NT * 128);
                 by_rows(R, [&](auto tiles) {
                     constexpr int M = decltype(tiles)::value;
-                    float part[4][M][4] = {};
-                    mma_rows(tiles, a.d, gr.len1, gr.pitch1, R, x_parts, part);
+                    float sum[M][4] = {};
+                    mma_rows(tiles, a.d, gr.len1, gr.pitch1, R, x_parts, sum);
 #pragma unroll
                     for (int n = 0; n < M; ++n) {
-                        float c[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) c[i] = part[0][n][i] + part[1][n][i];
-                        *reinterpret_cast<float2*>(mine + n * 128 + g * 8 + 2 * t) = make_float2(c[0], c[1]);
-                        *reinterpret_cast<float2*>(mine + n * 128 + (g + 8) * 8 + 2 * t) = make_float2(c[2], c[3]);
+                        *reinterpret_cast<float2*>(mine + n * 128 + g * 8 + 2 * t) = make_float2(sum[n][0], sum[n][1]);
+                        *reinterpret_cast<float2*>(mine + n * 128 + (g + 8) * 8 + 2 * t) =
+                            make_float2(sum[n][2], sum[n][3]);
                     }
                 });
                 consumer_sync();
@@ -813,8 +822,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                     float* mine = yacc + warp * (NT * 8 * kFewRows);
                     by_rows(R, [&](auto tiles) {
                         constexpr int M = decltype(tiles)::value;
-                        float part[4][M][4] = {};
-                        mma_rows(tiles, gr.F, gr.len2, gr.pitch2, R, h_parts, part);
+                        float sum[M][4] = {};
+                        mma_rows(tiles, gr.F, gr.len2, gr.pitch2, R, h_parts, sum);
 #pragma unroll
                         for (int n = 0; n < M; ++n)
 #pragma unroll
@@ -823,12 +832,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                                 if (r < R) {
                                     const int tk = routed ? S.row_tok[row0 + r] : r;
                                     const float wt = routed ? S.row_w[row0 + r] : 1.f;
-                                    const float lo =
-                                        (part[0][n][i] + part[1][n][i]) + (part[2][n][i] + part[3][n][i]);
-                                    const float hi = (part[0][n][2 + i] + part[1][n][2 + i]) +
-                                                     (part[2][n][2 + i] + part[3][n][2 + i]);
-                                    mine[tk * kFewRows + g] += wt * lo;
-                                    mine[tk * kFewRows + g + 8] += wt * hi;
+                                    mine[tk * kFewRows + g] += wt * sum[n][i];
+                                    mine[tk * kFewRows + g + 8] += wt * sum[n][2 + i];
                                 }
                             }
                     });
