@@ -659,7 +659,7 @@ MOE_API moe_status moe_backward_check(const moe_params* p, const void* bws, moe_
  * CUDA cores.  Same inputs give the same bits without W; with W the projection
  * may split K over CTAs (fp32 additions in any order).
  * Constraints: d_in, d_out and r multiples of 8, r <= 128, n_adapters <= 1024,
- * N < 2^30 (fp32 with W: N <= 65535 * 64); else MOE_ERR_UNSUPPORTED.  Pointers
+ * d_in and d_out <= 2^23, N < 2^30 (fp32 with W: N <= 65535 * 64); else MOE_ERR_UNSUPPORTED.  Pointers
  * of x, W, A, B, base, y, dy, dx, dA, dB and ws 16-byte aligned.
  * An id outside -1 .. n_adapters - 1 counts as -1 and is reported by
  * moe_adapter_check.  N = 0 writes nothing (backward: zeroes dA and dB).

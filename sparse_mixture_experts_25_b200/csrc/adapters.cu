@@ -55,7 +55,6 @@ constexpr int kGradRows = 32;      // tokens of a grad stage
 constexpr int kGradFlush = 4;      // grad stages between additions to the sums
 constexpr int kFewN = 32;          // batches of the few-token form
 constexpr int kMaxSlices = 8;      // K slices of a shrink (CTAs of a cluster)
-constexpr int kMaxSplits = 8;      // token splits of a grad
 
 // bf16 parts of an operand: of type T itself, and of an fp32 one beside T
 template <typename T>
@@ -113,11 +112,13 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t (&out)[P]) {
     for (int i = 0; i < P; ++i) {
         out[i] = pack2(a, b);
         if (i + 1 < P) {
-            const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&out[i]);
-            a -= __bfloat162float(v.x);
-            b -= __bfloat162float(v.y);
-            if (!isfinite(a)) a = 0.f;
-            if (!isfinite(b)) b = 0.f;
+            a -= __uint_as_float(out[i] << 16);
+            b -= __uint_as_float(out[i] & 0xffff0000u);
+            const float both = a + b;
+            if (both != both) {  // one was not finite (rare)
+                a = isfinite(a) ? a : 0.f;
+                b = isfinite(b) ? b : 0.f;
+            }
         }
     }
 }
@@ -280,13 +281,13 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t* ids, 
 // shrink: out[pos, q] = s_a sum_k X[tok(pos), k] M_a(q, k) as parts.
 //   NN = false: M_a is A_a [r, K] (x -> u);  NN = true: M_a is B_a [K, r] (dy -> v)
 // A CTA has one tile and one of the cluster's K slices.  Stages of 64 K come
-// through a ring of asynchronous copies (the rows are gathered there).  With
-// ranks up to 64 a warp has 32 rows and one of a stage's two steps of 32 K, so
-// each adapter element read from shared memory meets 32 rows; above, 16 rows
-// and both steps.  A lane reads 8 consecutive K elements of a row and feeds
-// them to two MMAs, the adapter's elements in the same order of K.  The
-// cluster's CTAs add their sums in slice order through distributed shared
-// memory.
+// through a ring of asynchronous copies (the rows are gathered there); each of
+// the 8 warps has 16 rows and one of a stage's two steps of 32 K.  (Four warps
+// of 32 rows read the adapter half as often from shared memory, but left two
+// warps a scheduler to hide everything behind.)  A lane reads 8 consecutive K
+// elements of a row and feeds them to two MMAs, the adapter's elements in the
+// same order of K.  The cluster's CTAs add their sums in slice order through
+// distributed shared memory.
 // ---------------------------------------------------------------------------
 struct ShrinkArgs {
     const void* X;
@@ -313,11 +314,12 @@ __host__ __device__ constexpr int shrink_stage(int r) {
     return kRows * shrink_x_pitch<TA>() + (NN ? kShrinkK : r) * shrink_m_pitch<T, NN>(r);
 }
 
+constexpr int kShrinkThreads = 256;
+constexpr int kShrinkFlush = 4;    // stages between additions to the sums
+
 template <typename T, typename TA, bool NN, int NQ>
-__global__ void __launch_bounds__(128) adapter_shrink_kernel(const __grid_constant__ ShrinkArgs a) {
+__global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(const __grid_constant__ ShrinkArgs a) {
     constexpr int PA = act_parts<TA, T>(), PB = Parts<T>::self, PF = Parts<T>::f32;
-    constexpr int MR = NQ <= 8 ? 2 : 1;   // 16-row tiles of a warp
-    constexpr int STEPS = MR == 2 ? 1 : 2;
     constexpr int kXPitch = shrink_x_pitch<TA>();
     extern __shared__ __align__(128) uint8_t smem[];
     const cg::cluster_group cluster = cg::this_cluster();
@@ -326,89 +328,100 @@ __global__ void __launch_bounds__(128) adapter_shrink_kernel(const __grid_consta
     if (tile.adapter >= a.n_adapters) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int r = a.r, m_pitch = shrink_m_pitch<T, NN>(r), stage_bytes = shrink_stage<T, TA, NN>(r);
-    const TA* X = static_cast<const TA*>(a.X);
-    const T* M = static_cast<const T*>(a.M) + (int64_t)tile.adapter * r * a.K;
-    // this thread's copies of a stage: 16-byte piece xp of rows xr, xr + XS, ...
-    constexpr int XPIECES = kShrinkK * (int)sizeof(TA) / 16, XS = 128 / XPIECES;
-    const int xp = tid % XPIECES, xr = tid / XPIECES;
-    const TA* row[kRows / XS];
-#pragma unroll
-    for (int i = 0; i < kRows / XS; ++i) {
-        const int q = xr + i * XS;
-        row[i] = q < tile.rows ? X + (int64_t)a.p.perm[tile.pos + q] * a.K : nullptr;
-    }
     const int k_beg = blockIdx.y * a.slice, k_end = min(a.K, k_beg + a.slice);
     const int chunks = k_beg < k_end ? (k_end - k_beg + kShrinkK - 1) / kShrinkK : 0;
-    auto fill = [&](int c) {
-        if (c < chunks) {
-            const uint32_t xs = smem_addr(smem) + c % kStages * stage_bytes, ms = xs + kRows * kXPitch;
-            const int kb = k_beg + c * kShrinkK;
-            const int k = kb + xp * (16 / (int)sizeof(TA));
+    // this thread's copies of a stage, each with a source that moves on by a
+    // stage.  X: 16-byte piece xp of rows xr, xr + XS, ... (zeros past the tile)
+    constexpr int XPIECES = kShrinkK * (int)sizeof(TA) / 16, XS = kShrinkThreads / XPIECES, XN = kRows / XS;
+    const int xp = tid % XPIECES, xr = tid / XPIECES, xk = xp * (16 / (int)sizeof(TA));
+    const TA* xsrc[XN];
+    bool xhave[XN];
 #pragma unroll
-            for (int i = 0; i < kRows / XS; ++i) {
-                const bool in = row[i] && k < k_end;
-                copy16(xs + (xr + i * XS) * kXPitch + xp * 16, in ? row[i] + k : X, in);
+    for (int i = 0; i < XN; ++i) {
+        const int q = xr + i * XS;
+        xhave[i] = q < tile.rows;
+        xsrc[i] = static_cast<const TA*>(a.X) + (xhave[i] ? (int64_t)a.p.perm[tile.pos + q] * a.K : 0) + k_beg + xk;
+    }
+    // M: pieces tid, tid + 256, ... of the [r][64] (NN: [64][r]) block
+    constexpr int E = 16 / (int)sizeof(T);
+    constexpr int MN = (NQ * 8 * kShrinkK / E + kShrinkThreads - 1) / kShrinkThreads;
+    const T* const M = static_cast<const T*>(a.M) + (int64_t)tile.adapter * r * a.K + (int64_t)k_beg * (NN ? r : 1);
+    const T* msrc[MN];
+    int mdst[MN], mk[MN];  // byte offset in the stage; first K of the piece (no such piece: past all)
+#pragma unroll
+    for (int i = 0; i < MN; ++i) {
+        const int per = NN ? r / E : kShrinkK / E, at = tid + i * kShrinkThreads, major = at / per, minor = at % per * E;
+        const bool have = major < (NN ? kShrinkK : r);
+        mk[i] = have ? (NN ? major : minor) : 1 << 30;
+        msrc[i] = M + (have ? (NN ? (int64_t)major * r : (int64_t)major * a.K) + minor : 0);
+        // NN: K rows in the order that puts the four lanes' rows next to one another
+        const int row = NN ? (major & 32) + (major & 7) * 4 + (major >> 3 & 3) : major;
+        mdst[i] = kRows * kXPitch + row * m_pitch + minor * (int)sizeof(T);
+    }
+    const uint32_t ring = smem_addr(smem), xdst = xr * kXPitch + xp * 16;
+    uint32_t to = ring;
+    int left = k_end - k_beg;  // K from the next stage to fill on
+    auto fill = [&]() {
+        if (left > 0) {
+            const bool whole = left >= kShrinkK;
+#pragma unroll
+            for (int i = 0; i < XN; ++i) {
+                const bool in = xhave[i] && (whole || xk < left);
+                copy16(to + xdst + i * XS * kXPitch, whole || in ? xsrc[i] : a.X, in);
+                xsrc[i] += kShrinkK;
             }
-            constexpr int E = 16 / (int)sizeof(T);  // elements of a piece
-            const int per = NN ? r / E : kShrinkK / E;
-            for (int i = tid; i < (NN ? kShrinkK : r) * per; i += 128) {
-                const int major = i / per, minor = i % per * E;
-                if (NN) {
-                    // K rows in the order that puts the four lanes' rows next to one another
-                    const int at = (major & 32) + (major & 7) * 4 + (major >> 3 & 3);
-                    const bool in = kb + major < k_end;
-                    copy16(ms + at * m_pitch + minor * (int)sizeof(T), in ? M + (int64_t)(kb + major) * r + minor : M, in);
-                } else {
-                    const bool in = kb + minor < k_end;
-                    copy16(ms + major * m_pitch + minor * (int)sizeof(T), in ? M + (int64_t)major * a.K + kb + minor : M, in);
-                }
+#pragma unroll
+            for (int i = 0; i < MN; ++i) {
+                const bool in = whole || mk[i] < left;
+                if (mk[i] < kShrinkK) copy16(to + mdst[i], in ? msrc[i] : M, in);
+                msrc[i] += NN ? kShrinkK * r : kShrinkK;
             }
+            left -= kShrinkK;
+            to = to + stage_bytes == ring + kStages * stage_bytes ? ring : to + stage_bytes;
         }
         copies_commit();
     };
 #pragma unroll
-    for (int c = 0; c < kStages - 1; ++c) fill(c);
-    const int row0 = MR == 2 ? (warp & 1) * 32 : warp * 16;
-    float sum[MR][NQ][4] = {};
+    for (int c = 0; c < kStages - 1; ++c) fill();
+    const int row0 = (warp & 3) * 16, step = warp >> 2;
+    float sum[NQ][4] = {}, acc[NQ][4] = {};
+    auto flush = [&]() {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum[n][e] += acc[n][e];
+                acc[n][e] = 0.f;
+            }
+    };
     for (int c = 0; c < chunks; ++c) {
         copies_wait<kStages - 2>();
         __syncthreads();
-        fill(c + kStages - 1);
+        fill();
         const uint8_t* xs = smem + c % kStages * stage_bytes;
         const uint8_t* ms = xs + kRows * kXPitch;
-        uint4 x[STEPS][MR][2][PA];
+        uint4 x[2][PA];
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-            for (int m = 0; m < MR; ++m)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    load8_parts<PA>(reinterpret_cast<const TA*>(xs + (row0 + m * 16 + g + 8 * i) * kXPitch) +
-                                        (MR == 2 ? warp >> 1 : s) * 32 + t * 8,
-                                    true, x[s][m][i]);
+        for (int i = 0; i < 2; ++i)
+            load8_parts<PA>(reinterpret_cast<const TA*>(xs + (row0 + g + 8 * i) * kXPitch) + step * 32 + t * 8, true, x[i]);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             if (n * 8 >= r) break;
-            uint4 b[STEPS][PB];
+            uint4 b[PB];
+            if constexpr (!NN) {
+                load8_parts<PB>(reinterpret_cast<const T*>(ms + (n * 8 + g) * m_pitch) + step * 32 + t * 8, true, b);
+            } else if constexpr (sizeof(T) == 2) {
+                const int m = lane >> 3, i = lane & 7;
+                uint32_t v[4];
+                ldmatrix_x4_trans(v, ms + (step * 32 + ((i & 1) + 2 * m) * 4 + (i >> 1)) * m_pitch + n * 16);
+                b[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            } else {
+                float v[8];
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int step = MR == 2 ? warp >> 1 : s;
-                if constexpr (!NN) {
-                    load8_parts<PB>(reinterpret_cast<const T*>(ms + (n * 8 + g) * m_pitch) + step * 32 + t * 8, true, b[s]);
-                } else if constexpr (sizeof(T) == 2) {
-                    const int m = lane >> 3, i = lane & 7;
-                    uint32_t v[4];
-                    ldmatrix_x4_trans(v, ms + (step * 32 + ((i & 1) + 2 * m) * 4 + (i >> 1)) * m_pitch + n * 16);
-                    b[s][0] = make_uint4(v[0], v[1], v[2], v[3]);
-                } else {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[e] = *reinterpret_cast<const float*>(ms + (step * 32 + e * 4 + t) * m_pitch + (n * 8 + g) * 4);
-                    split8<PB>(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), b[s]);
-                }
+                for (int e = 0; e < 8; ++e)
+                    v[e] = *reinterpret_cast<const float*>(ms + (step * 32 + e * 4 + t) * m_pitch + (n * 8 + g) * 4);
+                split8<PB>(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), b);
             }
-            float acc[MR][4] = {};
             // small products first
 #pragma unroll
             for (int level = (PA > PB ? PA : PB) - 1; level >= 0; --level)
@@ -416,44 +429,35 @@ __global__ void __launch_bounds__(128) adapter_shrink_kernel(const __grid_consta
                 for (int j = 0; j < PB; ++j) {
                     const int i = level - j;
                     if (i < 0 || i >= PA) continue;
-#pragma unroll
-                    for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-                        for (int m = 0; m < MR; ++m) {
-                            const uint4 &lo = x[s][m][0][i], &hi = x[s][m][1][i];
-                            mma_bf16(acc[m], lo.x, hi.x, lo.y, hi.y, b[s][j].x, b[s][j].y);
-                            mma_bf16(acc[m], lo.z, hi.z, lo.w, hi.w, b[s][j].z, b[s][j].w);
-                        }
+                    const uint4 &lo = x[0][i], &hi = x[1][i];
+                    mma_bf16(acc[n], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
+                    mma_bf16(acc[n], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
                 }
-#pragma unroll
-            for (int m = 0; m < MR; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum[m][n][e] += acc[m][e];
         }
+        if (c % kShrinkFlush == kShrinkFlush - 1) flush();
     }
+    flush();
     // the cluster's sums, slice by slice (and step by step), then the parts
     copies_wait<0>();
     __syncthreads();
-    float* mine = reinterpret_cast<float*>(smem);  // [MR][64][r]
+    float* mine = reinterpret_cast<float*>(smem);  // [2 steps][64][r]
 #pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            if (n * 8 >= r) break;
-            const int at = ((MR == 2 ? warp >> 1 : 0) * kRows + row0 + m * 16 + g) * r + n * 8 + 2 * t;
-            *reinterpret_cast<float2*>(mine + at) = make_float2(sum[m][n][0], sum[m][n][1]);
-            *reinterpret_cast<float2*>(mine + at + 8 * r) = make_float2(sum[m][n][2], sum[m][n][3]);
-        }
+    for (int n = 0; n < NQ; ++n) {
+        if (n * 8 >= r) break;
+        const int at = (step * kRows + row0 + g) * r + n * 8 + 2 * t;
+        *reinterpret_cast<float2*>(mine + at) = make_float2(sum[n][0], sum[n][1]);
+        *reinterpret_cast<float2*>(mine + at + 8 * r) = make_float2(sum[n][2], sum[n][3]);
+    }
     cluster.sync();
     const int slices = cluster.num_blocks(), rank = cluster.block_rank();
     const float scale = a.scale[tile.adapter];
     const int pairs = tile.rows * r / 2;
-    for (int i = rank * 128 + tid; i < pairs; i += 128 * slices) {
+    for (int i = rank * kShrinkThreads + tid; i < pairs; i += kShrinkThreads * slices) {
         float2 s = make_float2(0.f, 0.f);
         for (int q = 0; q < slices; ++q) {
             const float* theirs = cluster.map_shared_rank(mine, q) + 2 * i;
 #pragma unroll
-            for (int m = 0; m < MR; ++m) {
+            for (int m = 0; m < 2; ++m) {
                 const float2 v = *reinterpret_cast<const float2*>(theirs + m * kRows * r);
                 s.x += v.x;
                 s.y += v.y;
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(128) adapter_shrink_kernel(const __grid_consta
 // parts of u in registers throughout, the span's part of the adapter in shared
 // memory.  Per 32 columns a lane has 8 consecutive ones of two rows (the four
 // MMA tiles take the columns in that order), so a row is read and written in
-// whole lines; what is added to is fetched one step ahead.
+// whole lines; what is added to is fetched two steps ahead.
 // ---------------------------------------------------------------------------
 struct ExpandArgs {
     const __nv_bfloat16* in;  // [parts][N][r]
@@ -498,8 +502,9 @@ __host__ __device__ constexpr int expand_part(int span) {
     return NN ? NK * 16 * (span * 2 + 16) : span * expand_pitch(NK * 16);
 }
 
+// four CTAs on an SM where the parts of u fit in their registers
 template <typename T, bool NN, int NK>
-__global__ void __launch_bounds__(128) adapter_expand_kernel(const __grid_constant__ ExpandArgs a) {
+__global__ void __launch_bounds__(128, Parts<T>::f32 * NK <= 8 ? 4 : 2) adapter_expand_kernel(const __grid_constant__ ExpandArgs a) {
     constexpr int PB = Parts<T>::self, PF = Parts<T>::f32;
     constexpr int R = NK * 16;
     const int pitch = NN ? a.span * 2 + 16 : expand_pitch(R), part_bytes = expand_part<T, NN, NK>(a.span);
@@ -582,57 +587,64 @@ __global__ void __launch_bounds__(128) adapter_expand_kernel(const __grid_consta
                 }
             }
     };
-    float4 next[2][2];
-    fetch(0, next);
+    float4 next[2][2][2];  // the next two steps'
+    fetch(0, next[0]);
+    fetch(32, next[1]);
     __syncthreads();
-#pragma unroll 1
+#pragma unroll 2
     for (int n0 = 0; n0 < cols; n0 += 32) {
         float4 add[2][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) add[i][h] = next[i][h];
-        if (n0 + 32 < cols) fetch(n0 + 32, next);
+            for (int h = 0; h < 2; ++h) {
+                add[i][h] = next[0][i][h];
+                next[0][i][h] = next[1][i][h];
+            }
+        fetch(n0 + 64, next[1]);
         float acc[4][4] = {};
         if (!none) {
 #pragma unroll
-            for (int level = (PF > PB ? PF : PB) - 1; level >= 0; --level)  // small products first
+            for (int s = 0; s < NK; ++s) {
+                uint32_t b[PB][4][2];
 #pragma unroll
                 for (int q = 0; q < PB; ++q) {
-                    const int j = level - q;
-                    if (j < 0 || j >= PF) continue;
+                    if (NN) {
+                        // two column tiles at a time: (b0, b1) of each
+                        const int m = lane >> 3, i = lane & 7;
+                        const uint8_t* p = smem + q * part_bytes +
+                                           (s * 16 + ((i & 1) + 2 * (m & 1)) * 4 + (i >> 1)) * pitch +
+                                           (n0 + (m >> 1) * 8) * 2;
 #pragma unroll
-                    for (int s = 0; s < NK; ++s) {
-                        uint32_t b[4][2];
-                        if (NN) {
-                            // two column tiles at a time: (b0, b1) of each
-                            const int m = lane >> 3, i = lane & 7;
-                            const uint8_t* p = smem + q * part_bytes +
-                                               (s * 16 + ((i & 1) + 2 * (m & 1)) * 4 + (i >> 1)) * pitch +
-                                               (n0 + (m >> 1) * 8) * 2;
+                        for (int h = 0; h < 2; ++h) {
                             uint32_t v[4];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                ldmatrix_x4_trans(v, p + h * 32);
-                                b[2 * h][0] = v[0];
-                                b[2 * h][1] = v[1];
-                                b[2 * h + 1][0] = v[2];
-                                b[2 * h + 1][1] = v[3];
-                            }
-                        } else {
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) {
-                                const uint2 v = *reinterpret_cast<const uint2*>(
-                                    smem + q * part_bytes + (n0 + n * 8 + g) * pitch + (s * 16 + 4 * t) * 2);
-                                b[n][0] = v.x;
-                                b[n][1] = v.y;
-                            }
+                            ldmatrix_x4_trans(v, p + h * 32);
+                            b[q][2 * h][0] = v[0];
+                            b[q][2 * h][1] = v[1];
+                            b[q][2 * h + 1][0] = v[2];
+                            b[q][2 * h + 1][1] = v[3];
                         }
+                    } else {
 #pragma unroll
-                        for (int n = 0; n < 4; ++n)
-                            mma_bf16(acc[n], u[j][s][0], u[j][s][1], u[j][s][2], u[j][s][3], b[n][0], b[n][1]);
+                        for (int n = 0; n < 4; ++n) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(
+                                smem + q * part_bytes + (n0 + n * 8 + g) * pitch + (s * 16 + 4 * t) * 2);
+                            b[q][n][0] = v.x;
+                            b[q][n][1] = v.y;
+                        }
                     }
                 }
+#pragma unroll
+                for (int level = (PF > PB ? PF : PB) - 1; level >= 0; --level)  // small products first
+#pragma unroll
+                    for (int q = 0; q < PB; ++q) {
+                        const int j = level - q;
+                        if (j < 0 || j >= PF) continue;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+                            mma_bf16(acc[n], u[j][s][0], u[j][s][1], u[j][s][2], u[j][s][3], b[q][n][0], b[q][n][1]);
+                    }
+            }
         }
         // tile n has columns 2 n, 2 n + 1 of this lane's 8
         if (n0 + 8 * t < cols) {
@@ -652,18 +664,24 @@ __global__ void __launch_bounds__(128) adapter_expand_kernel(const __grid_consta
 // ---------------------------------------------------------------------------
 // grad: G_a(q, j) = sum over adapter a's tokens of in[pos, q] Z[tok(pos), j]
 //   TRANS = false: dA_a [r, J] from v and x;  TRANS = true: dB_a [J, r] from u and dy
-// A CTA has one adapter, 128 columns and one split of the tokens; each warp 32
-// of the columns and all ranks.  The tokens' parts of u or v, which all warps
-// need, and their places come through a ring of asynchronous copies; a row of Z
-// is used by one warp only and goes from global memory to its registers a
-// stage ahead: a lane reads 4 consecutive columns of four rows, and the four MMA
-// tiles take the columns in that order, so a lane's results are 8 consecutive
-// columns too.
+// A CTA has 128 columns and a range of the sorted tokens, the same for every CTA
+// of the row whatever the adapters' shares (cut by adapter instead, the largest
+// one's CTAs ran alone at the end: 143 against XX us for dB of 8192 tokens of
+// four uneven adapters, r = 64, d = 4096).  An adapter that lies in one range is
+// written to its place; one that continues in others leaves partial sums, at
+// most one per range and adapter met, which the reduction adds in order.  Each
+// warp has 32 of the columns and all ranks.  The tokens' parts of u or v, which
+// all warps need, and their places come through a ring of asynchronous copies;
+// a row of Z is used by one warp only and goes from global memory to its
+// registers a stage ahead: a lane reads 4 consecutive columns of four rows, and
+// the four MMA tiles take the columns in that order, so a lane's results are 8
+// consecutive columns too.
 // ---------------------------------------------------------------------------
 struct GradArgs {
     const __nv_bfloat16* in;  // [parts][N][r]
     const void* Z;
-    float* out;               // [n_adapters][r J], or partial sums [splits][n_adapters][r J]
+    float* out;               // [n_adapters][r J]
+    float* part;              // [ranges + n_adapters][r J]: partial sum of adapter a in range i at i + a
     int J, r, n_adapters;
     int64_t N;
     Plan p;
@@ -710,144 +728,182 @@ __global__ void __launch_bounds__(128) adapter_grad_kernel(const __grid_constant
     extern __shared__ __align__(128) uint8_t smem[];
     float* sums = reinterpret_cast<float*>(smem + kStages * kStage);  // [MT * 16][128 threads]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int adapter = blockIdx.y, splits = gridDim.z, split = blockIdx.z;
     const int r = a.r, J = a.J;
-    const int seg0 = a.p.seg[adapter], seg1 = a.p.seg[adapter + 1];
-    const int all = (seg1 - seg0 + kGradRows - 1) / kGradRows;
-    const int c0 = (int)((int64_t)all * split / splits), c1 = (int)((int64_t)all * (split + 1) / splits);
+    const int tokens = a.p.seg[a.n_adapters];  // those that have an adapter
+    const int lo = (int)((int64_t)tokens * blockIdx.y / gridDim.y), hi = (int)((int64_t)tokens * (blockIdx.y + 1) / gridDim.y);
+    if (lo >= hi) return;
     const int col = blockIdx.x * kGradCols + warp * 32 + 4 * g;  // this lane's columns of Z
     const TZ* Z = static_cast<const TZ*>(a.Z) + col;
     const bool col_in = col < J;
-    auto fill = [&](int c) {
-        if (c < c1) {
-            const uint32_t st = smem_addr(smem) + (c - c0) % kStages * kStage;
-            const int pos = seg0 + c * kGradRows;
-            for (int i = tid; i < kGradRows * MT * 2; i += 128) {
-                const int row = i / (MT * 2), q = i % (MT * 2) * 8;
-                const bool in = pos + row < seg1 && q < r;
-#pragma unroll
-                for (int j = 0; j < PF; ++j)
-                    copy16(st + j * kInPart + row * kInPitch + q * 2,
-                           in ? a.in + ((int64_t)j * a.N + pos + row) * r + q : a.in, in);
-            }
-            if (tid < kGradRows)  // 4 bytes each: the places need not be 16-byte aligned
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(st + PF * kInPart + tid * 4),
-                             "l"(a.p.perm + (pos + tid < seg1 ? pos + tid : 0)), "r"(pos + tid < seg1 ? 4 : 0)
-                             : "memory");
-        }
-        copies_commit();
-    };
-    // rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of each step of 16 tokens
-    auto fetch = [&](int c, Raw4<TZ> (&z)[STEPS][4]) {
-        const int32_t* tok = reinterpret_cast<const int32_t*>(smem + (c - c0) % kStages * kStage + PF * kInPart);
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = s * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
-                if (col_in && seg0 + c * kGradRows + row < seg1) z[s][i].load(Z + (int64_t)tok[row] * J);
-                else z[s][i].zero();
-            }
-    };
-#pragma unroll
-    for (int c = 0; c < kStages - 1; ++c) fill(c0 + c);
-    float acc[MT][4][4] = {};
-    auto flush = [&](bool first, bool last) {
-#pragma unroll
-        for (int i = 0; i < MT * 16; ++i) {
-            float& v = acc[i / 16][i / 4 % 4][i % 4];
-            if (!first) v += sums[i * 128 + tid];
-            if (!last) {
-                sums[i * 128 + tid] = v;
-                v = 0.f;
-            }
-        }
-    };
-    Raw4<TZ> z[STEPS][4];
-    if (c0 < c1) {
-        copies_wait<kStages - 2>();
-        __syncthreads();
-        fetch(c0, z);
+    // the adapter of position lo: the last one that begins at or before it
+    int adapter = 0;
+    for (int top = a.n_adapters - 1; adapter < top;) {
+        const int mid = (adapter + top + 1) >> 1;
+        if (a.p.seg[mid] <= lo) adapter = mid;
+        else top = mid - 1;
     }
-    bool first = true;
-    for (int c = c0; c < c1; ++c) {
-        copies_wait<kStages - 3>();  // this stage and the next
-        __syncthreads();
-        fill(c + kStages - 1);
-        Raw4<TZ> ahead[STEPS][4];
-        if (c + 1 < c1) fetch(c + 1, ahead);
-        const uint8_t* st = smem + (c - c0) % kStages * kStage;
+    // this thread's pieces of a stage: 8 ranks of rows ir, ir + IS, ...
+    constexpr int IP = MT * 2, IS = 128 / IP, IN = (kGradRows + IS - 1) / IS;
+    const int iq = tid % IP * 8, ir = tid / IP;
+    for (int beg = lo; beg < hi; ++adapter) {
+        const int seg0 = a.p.seg[adapter], seg_end = a.p.seg[adapter + 1];
+        if (seg_end <= beg) continue;  // an adapter without tokens
+        const int seg1 = min(seg_end, hi), c0 = 0, c1 = (seg1 - beg + kGradRows - 1) / kGradRows;
+        auto fill = [&](int c) {
+            if (c < c1) {
+                const uint32_t st = smem_addr(smem) + c % kStages * kStage;
+                const int pos = beg + c * kGradRows;
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int m = lane >> 3, i = lane & 7;
-            uint32_t b[4][2][PZ];
+                for (int i = 0; i < IN; ++i) {
+                    const int row = ir + i * IS;
+                    if (row >= kGradRows) break;
+                    const bool in = pos + row < seg1 && iq < r;
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+                    for (int j = 0; j < PF; ++j)
+                        copy16(st + j * kInPart + row * kInPitch + iq * 2,
+                               in ? a.in + ((int64_t)j * a.N + pos + row) * r + iq : a.in, in);
+                }
+                if (tid < kGradRows)  // 4 bytes each: the places need not be 16-byte aligned
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(st + PF * kInPart + tid * 4),
+                                 "l"(a.p.perm + (pos + tid < seg1 ? pos + tid : 0)), "r"(pos + tid < seg1 ? 4 : 0)
+                                 : "memory");
+            }
+            copies_commit();
+        };
+        // rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of each step of 16 tokens
+        auto fetch = [&](int c, Raw4<TZ> (&z)[STEPS][4]) {
+            const int32_t* tok = reinterpret_cast<const int32_t*>(smem + c % kStages * kStage + PF * kInPart);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) pair_parts<PZ>(z[s][2 * h], z[s][2 * h + 1], n, b[n][h]);
+            for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+                for (int i = 0; i < 4; ++i) {
+                    const int row = s * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+                    if (col_in && beg + c * kGradRows + row < seg1) z[s][i].load(Z + (int64_t)tok[row] * J);
+                    else z[s][i].zero();
+                }
+        };
 #pragma unroll
-                for (int j = PF - 1; j >= 0; --j) {
-                    // A: (m 0-7, k 0-7), (m 8-15, k 0-7), (m 0-7, k 8-15), (m 8-15, k 8-15)
-                    uint32_t v[4];
-                    ldmatrix_x4_trans(v, st + j * kInPart + (s * 16 + (m >> 1) * 8 + i) * kInPitch +
-                                             (mt * 16 + (m & 1) * 8) * 2);
+        for (int c = 0; c < kStages - 1; ++c) fill(c0 + c);
+        float acc[MT][4][4] = {};
+        auto flush = [&](bool first, bool last) {
 #pragma unroll
-                    for (int q = PZ - 1; q >= 0; --q) {
-                        if (!counts<PF, PZ>(j, q)) continue;
+            for (int i = 0; i < MT * 16; ++i) {
+                float& v = acc[i / 16][i / 4 % 4][i % 4];
+                if (!first) v += sums[i * 128 + tid];
+                if (!last) {
+                    sums[i * 128 + tid] = v;
+                    v = 0.f;
+                }
+            }
+        };
+        Raw4<TZ> z[STEPS][4];
+        if (c0 < c1) {
+            copies_wait<kStages - 2>();
+            __syncthreads();
+            fetch(c0, z);
+        }
+        bool first = true;
+        for (int c = c0; c < c1; ++c) {
+            copies_wait<kStages - 3>();  // this stage and the next
+            __syncthreads();
+            fill(c + kStages - 1);
+            Raw4<TZ> ahead[STEPS][4];
+            if (c + 1 < c1) fetch(c + 1, ahead);
+            const uint8_t* st = smem + c % kStages * kStage;
 #pragma unroll
-                        for (int n = 0; n < 4; ++n)
-                            mma_bf16(acc[mt][n], v[0], v[1], v[2], v[3], b[n][0][q], b[n][1][q]);
+            for (int s = 0; s < STEPS; ++s) {
+                const int m = lane >> 3, i = lane & 7;
+                uint32_t b[4][2][PZ];
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) pair_parts<PZ>(z[s][2 * h], z[s][2 * h + 1], n, b[n][h]);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                    for (int j = PF - 1; j >= 0; --j) {
+                        // A: (m 0-7, k 0-7), (m 8-15, k 0-7), (m 0-7, k 8-15), (m 8-15, k 8-15)
+                        uint32_t v[4];
+                        ldmatrix_x4_trans(v, st + j * kInPart + (s * 16 + (m >> 1) * 8 + i) * kInPitch +
+                                                 (mt * 16 + (m & 1) * 8) * 2);
+#pragma unroll
+                        for (int q = PZ - 1; q >= 0; --q) {
+                            if (!counts<PF, PZ>(j, q)) continue;
+#pragma unroll
+                            for (int n = 0; n < 4; ++n)
+                                mma_bf16(acc[mt][n], v[0], v[1], v[2], v[3], b[n][0][q], b[n][1][q]);
+                        }
                     }
                 }
             }
-        }
-        if ((c - c0) % kGradFlush == kGradFlush - 1 && c + 1 < c1) {
-            flush(first, false);
-            first = false;
-        }
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[s][i] = ahead[s][i];
-    }
-    flush(first, true);
-    copies_wait<0>();
-    // tile n has columns 8 t + n and 8 t + 4 + n of the warp's 32
-    float* out = a.out + ((int64_t)split * a.n_adapters + adapter) * r * J;
-    const int j = blockIdx.x * kGradCols + warp * 32 + 8 * t;
-    if (j >= J) return;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int q = mt * 16 + g + 8 * h;
-            if (q >= r) continue;
-            if (TRANS) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) out[(int64_t)(j + e) * r + q] = acc[mt][e & 3][2 * h + (e >> 2)];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<float4*>(out + (int64_t)q * J + j + 4 * e) =
-                        make_float4(acc[mt][0][2 * h + e], acc[mt][1][2 * h + e], acc[mt][2][2 * h + e],
-                                    acc[mt][3][2 * h + e]);
+            if (c % kGradFlush == kGradFlush - 1 && c + 1 < c1) {
+                flush(first, false);
+                first = false;
             }
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[s][i] = ahead[s][i];
         }
+        flush(first, true);
+        copies_wait<0>();
+        __syncthreads();  // the ring is the next adapter's
+        // tile n has columns 8 t + n and 8 t + 4 + n of the warp's 32
+        const bool alone = seg0 >= lo && seg_end <= hi;
+        float* out = alone ? a.out + (int64_t)adapter * r * J : a.part + ((int64_t)blockIdx.y + adapter) * r * J;
+        beg = seg1;
+        const int j = blockIdx.x * kGradCols + warp * 32 + 8 * t;
+        if (j < J) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int q = mt * 16 + g + 8 * h;
+                    if (q >= r) continue;
+                    if (TRANS) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) out[(int64_t)(j + e) * r + q] = acc[mt][e & 3][2 * h + (e >> 2)];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float4*>(out + (int64_t)q * J + j + 4 * e) =
+                                make_float4(acc[mt][0][2 * h + e], acc[mt][1][2 * h + e], acc[mt][2][2 * h + e],
+                                            acc[mt][3][2 * h + e]);
+                    }
+                }
+        }
+    }
 }
 
-__global__ void __launch_bounds__(256) adapter_reduce_kernel(const float4* part, int splits, int64_t n4, float4* out) {
+// What the ranges left: an adapter's partial sums, range by range, zeros for one
+// without tokens.  CTA (i, a): some of adapter a's elements.
+__global__ void __launch_bounds__(256)
+    adapter_reduce_kernel(const float4* part, const int32_t* seg, int n_adapters, int ranges, int64_t n4, float4* out) {
+    const int adapter = blockIdx.y, seg0 = seg[adapter], seg1 = seg[adapter + 1];
+    const int64_t tokens = seg[n_adapters];
+    float4* to = out + (int64_t)adapter * n4;
+    int first = 0, last = -1;
+    if (seg0 < seg1) {
+        // the ranges of its first and last token; range i ends at tokens (i + 1) / ranges
+        auto range_of = [&](int64_t pos) {
+            int i = (int)(pos * ranges / tokens);
+            while (tokens * (i + 1) / ranges <= pos) ++i;
+            return i;
+        };
+        first = range_of(seg0);
+        last = range_of(seg1 - 1);
+        if (first == last) return;  // written where it was summed
+    }
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
-        float4 s = part[i];
-        for (int q = 1; q < splits; ++q) {
-            const float4 v = part[(int64_t)q * n4 + i];
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = first; q <= last; ++q) {
+            const float4 v = part[((int64_t)q + adapter) * n4 + i];
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
             s.w += v.w;
         }
-        out[i] = s;
+        to[i] = s;
     }
 }
 
@@ -991,11 +1047,11 @@ int few_slices(int64_t N, int K) {
     return (int)std::max<int64_t>(1, std::min<int64_t>({16, 2 * num_sms() / std::max<int64_t>(N, 1), K / 256}));
 }
 
-// token splits of a grad, whose partial sums a reduction adds in order
-int grad_splits(const moe_adapter_params& p, int J) {
-    const int64_t ctas = (int64_t)((J + kGradCols - 1) / kGradCols) * p.n_adapters;
-    const int64_t want = (4 * (int64_t)num_sms() + ctas - 1) / ctas;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, want, p.N / 256}));
+// ranges of tokens of a grad: as many as fit on the GPU at once (three CTAs on an
+// SM) with the columns' CTAs, at least 64 tokens each
+int grad_ranges(const moe_adapter_params& p, int J) {
+    const int64_t cols = (J + kGradCols - 1) / kGradCols;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(3 * (int64_t)num_sms() / cols, p.N / 64));
 }
 
 struct Layout {
@@ -1025,9 +1081,11 @@ Layout layout_of(const moe_adapter_params& p, bool with_W, bool backward) {
             L.hi = take(N * (size_t)p.d_out * 2);
             L.lo = take(N * (size_t)p.d_out * 2);
         }
-        const int sa = grad_splits(p, p.d_in), sb = grad_splits(p, p.d_out);
-        const size_t pa = sa > 1 ? (size_t)sa * p.d_in : 0, pb = sb > 1 ? (size_t)sb * p.d_out : 0;
-        L.part = take(std::max(pa, pb) * (size_t)p.n_adapters * r * 4);
+        // partial sums of at most a range's last adapter and the next one's first, so
+        // (ranges + adapters) of them; never written with one range
+        const size_t ra = grad_ranges(p, p.d_in), rb = grad_ranges(p, p.d_out);
+        const size_t pa = ra > 1 ? (ra + p.n_adapters) * p.d_in : 0, pb = rb > 1 ? (rb + p.n_adapters) * p.d_out : 0;
+        L.part = take(std::max(pa, pb) * r * 4);
     }
     L.total = off;
     return L;
@@ -1064,7 +1122,7 @@ cudaError_t launch_shrink_q(const moe_adapter_params& p, ShrinkArgs a, cudaStrea
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)tile_bound(p), (unsigned)slices, 1);
-    cfg.blockDim = dim3(128, 1, 1);
+    cfg.blockDim = dim3(kShrinkThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1100,13 +1158,13 @@ cudaError_t launch_shrink(const moe_adapter_params& p, const TA* X, const T* M, 
 template <typename T, bool NN, int NK>
 cudaError_t launch_expand_k(const moe_adapter_params& p, ExpandArgs a, cudaStream_t st) {
     constexpr auto kern = adapter_expand_kernel<T, NN, NK>;
-    // columns of a CTA: at most what leaves room for two CTAs on an SM, and few
+    // columns of a CTA: at most what leaves room for five CTAs on an SM, and few
     // enough that there are CTAs for two waves
     const int64_t tiles = p.N / kRows + 1;
     auto smem = [](int span) { return (size_t)Parts<T>::self * expand_part<T, NN, NK>(span); };
     static_assert((size_t)Parts<T>::self * expand_part<T, NN, NK>(128) <= 232448, "shared memory per CTA");
     a.span = 512;
-    while (a.span > 128 && (smem(a.span) > 100 * 1024 || tiles * ((a.J + a.span - 1) / a.span) < 2 * num_sms())) a.span /= 2;
+    while (a.span > 128 && (smem(a.span) > 40 * 1024 || tiles * ((a.J + a.span - 1) / a.span) < 2 * num_sms())) a.span /= 2;
     cudaError_t e = allow_smem_once<kern>(std::max(smem(128), (size_t)100 * 1024));
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)tile_bound(p), (unsigned)((a.J + a.span - 1) / a.span), 1);
@@ -1148,25 +1206,28 @@ cudaError_t launch_grad_m(const GradArgs& a, dim3 grid, cudaStream_t st) {
 template <typename T, typename TZ, bool TRANS>
 cudaError_t launch_grad(const moe_adapter_params& p, const __nv_bfloat16* in, const TZ* Z, int J, float* out,
                         float* part, const Plan& plan, cudaStream_t st) {
-    const int splits = grad_splits(p, J);
+    const int ranges = grad_ranges(p, J);
     GradArgs a{};
     a.in = in;
     a.Z = Z;
-    a.out = splits > 1 ? part : out;
+    a.out = out;
+    a.part = part;
     a.J = J;
     a.r = p.r;
     a.n_adapters = p.n_adapters;
     a.N = p.N;
     a.p = plan;
-    const dim3 grid((unsigned)((J + kGradCols - 1) / kGradCols), (unsigned)p.n_adapters, (unsigned)splits);
+    const dim3 grid((unsigned)((J + kGradCols - 1) / kGradCols), (unsigned)ranges);
     cudaError_t e = p.r <= 16   ? launch_grad_m<T, TZ, TRANS, 1>(a, grid, st)
                     : p.r <= 32 ? launch_grad_m<T, TZ, TRANS, 2>(a, grid, st)
                     : p.r <= 64 ? launch_grad_m<T, TZ, TRANS, 4>(a, grid, st)
                                 : launch_grad_m<T, TZ, TRANS, 8>(a, grid, st);
-    if (e != cudaSuccess || splits == 1) return e;
-    const int64_t n4 = (int64_t)p.n_adapters * p.r * J / 4;
-    adapter_reduce_kernel<<<(unsigned)min64((n4 + 255) / 256, (int64_t)num_sms() * 8), 256, 0, st>>>(
-        reinterpret_cast<const float4*>(part), splits, n4, reinterpret_cast<float4*>(out));
+    if (e != cudaSuccess) return e;
+    // a CTA for 1024 of an adapter's elements, fewer where there are many adapters
+    const int64_t n4 = (int64_t)p.r * J / 4;
+    const int64_t blocks = std::min<int64_t>((n4 + 255) / 256, std::max<int64_t>(1, 8 * (int64_t)num_sms() / p.n_adapters));
+    adapter_reduce_kernel<<<dim3((unsigned)blocks, (unsigned)p.n_adapters), 256, 0, st>>>(
+        reinterpret_cast<const float4*>(part), plan.seg, p.n_adapters, ranges, n4, reinterpret_cast<float4*>(out));
     return cudaGetLastError();
 }
 
@@ -1268,8 +1329,9 @@ moe_status check(const moe_adapter_params* p) {
         record_error("moe_adapter: d_in, d_out and r must be multiples of 8");
         return MOE_ERR_UNSUPPORTED;
     }
-    if (p->r > kMaxAdapterRank || p->n_adapters > kMaxAdapters || p->N >= (int64_t)1 << 30) {
-        record_error("moe_adapter: at most rank 128, 1024 adapters and 2^30 - 1 tokens");
+    if (p->r > kMaxAdapterRank || p->n_adapters > kMaxAdapters || p->N >= (int64_t)1 << 30 || p->d_in > 1 << 23 ||
+        p->d_out > 1 << 23) {
+        record_error("moe_adapter: at most rank 128, 1024 adapters, 2^30 - 1 tokens and widths of 2^23");
         return MOE_ERR_UNSUPPORTED;
     }
     return MOE_OK;
