@@ -81,7 +81,7 @@ struct Plan {
     int32_t* seg;       // [n_adapters + 2] first position of each adapter; tokens without one last
     Tile* tiles;        // tiles of at most kRows rows, one adapter each
     int32_t* n_tiles;
-    int32_t* one_group; // {0, N} and {0, ceil(N / 128)}: the dense W^T dy as a group of rows
+    int32_t* one_group; // {0, N}, {0, ceil(N / 128)}, {0, ceil(N / 256)}: all rows as one group of the GEMMs
     unsigned long long* counters;
 };
 
@@ -245,6 +245,8 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t* ids, 
             p.one_group[1] = N;
             p.one_group[2] = 0;
             p.one_group[3] = (N + 127) / 128;
+            p.one_group[4] = 0;
+            p.one_group[5] = (N + 255) / 256;
         }
     }
     __syncthreads();
@@ -477,16 +479,17 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(const __
 //   NN = false: M_a is B_a [J, r] (u -> y);  NN = true: M_a is A_a [r, J] (v -> dx)
 // A CTA has one tile and a span of columns; each warp 16 of the rows, their
 // parts of u in registers throughout, the span's part of the adapter in shared
-// memory.  Per 32 columns a lane has 8 consecutive ones of two rows (the four
-// MMA tiles take the columns in that order), so a row is read and written in
-// whole lines; what is added to is fetched two steps ahead.
+// memory.  Of 32 columns a lane has 4 t .. 4 t + 3 and the same 16 further on, of
+// two rows (the four MMA tiles take the columns in that order), so a row is read
+// and written in 64 consecutive bytes; what is added to is fetched two steps
+// ahead.
 // ---------------------------------------------------------------------------
 struct ExpandArgs {
     const __nv_bfloat16* in;  // [parts][N][r]
     const void* M;
-    const float* base;        // nullable; may be out
+    const float* base;        // nullable; may be out (what a projection left there counts as base)
+    const float* base2;       // nullable: added too
     float* out;
-    int add_out;              // 1: out already holds the projection
     int J, r, n_adapters, span;
     int64_t N;
     Plan p;
@@ -502,9 +505,9 @@ __host__ __device__ constexpr int expand_part(int span) {
     return NN ? NK * 16 * (span * 2 + 16) : span * expand_pitch(NK * 16);
 }
 
-// four CTAs on an SM where the parts of u fit in their registers
+// as many CTAs on an SM as the parts of u leave registers for
 template <typename T, bool NN, int NK>
-__global__ void __launch_bounds__(128, Parts<T>::f32 * NK <= 8 ? 4 : 2) adapter_expand_kernel(const __grid_constant__ ExpandArgs a) {
+__global__ void __launch_bounds__(128, Parts<T>::f32 * NK <= 4 ? 4 : Parts<T>::f32 * NK <= 8 ? 3 : 2) adapter_expand_kernel(const __grid_constant__ ExpandArgs a) {
     constexpr int PB = Parts<T>::self, PF = Parts<T>::f32;
     constexpr int R = NK * 16;
     const int pitch = NN ? a.span * 2 + 16 : expand_pitch(R), part_bytes = expand_part<T, NN, NK>(a.span);
@@ -512,42 +515,54 @@ __global__ void __launch_bounds__(128, Parts<T>::f32 * NK <= 8 ? 4 : 2) adapter_
     if ((int)blockIdx.x >= *a.p.n_tiles) return;
     const Tile tile = a.p.tiles[blockIdx.x];
     const bool none = tile.adapter >= a.n_adapters;
-    // tokens without an adapter: base (and what out holds) alone
-    if (none && (a.add_out ? a.base == nullptr : a.base == a.out)) return;
+    // tokens without an adapter: base alone
+    if (none && a.base == a.out && !a.base2) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int r = a.r, J = a.J;
     const T* M = static_cast<const T*>(a.M) + (none ? 0 : (int64_t)tile.adapter * r * J);
     const int jb = blockIdx.y * a.span, cols = min(a.span, J - jb);
-    // place of column j among the span's: the four tiles of 32 columns take pairs in turn
-    auto place = [](int j) { return (j & ~31) + (j >> 1 & 3) * 8 + (j >> 3 & 3) * 2 + (j & 1); };
+    // place of column j among the span's: tiles 0 and 1 (of 16 columns on: 2 and 3) take pairs in turn
+    auto place = [](int j) { return (j & ~15) + (j >> 1 & 1) * 8 + (j >> 2 & 3) * 2 + (j & 1); };
     if (!none) {
-        const int groups = (cols + 31) / 32 * 32;
-        if (NN) {
-            for (int i = tid; i < R * (groups / 8); i += 128) {
-                const int k = i / (groups / 8), j = i % (groups / 8) * 8;
-                uint4 v[PB];
-                load8_parts<PB>(M + (int64_t)k * J + jb + j, k < r && j < cols, v);
-                // K rows in the order that puts the four lanes' rows next to one another
-                uint8_t* at = smem + ((k & ~15) + (k & 3) * 4 + (k >> 2 & 3)) * pitch + place(j) * 2;
+        // 128 columns at a time, this thread's 2 NK pieces of 8 elements together
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 128) {
+            uint4 v[2 * NK][PB];
+            if (NN) {
+                const int j = c + tid % 16 * 8, k0 = tid / 16;
 #pragma unroll
-                for (int q = 0; q < PB; ++q) {
-                    *reinterpret_cast<uint32_t*>(at + q * part_bytes) = v[q].x;
-                    *reinterpret_cast<uint32_t*>(at + q * part_bytes + 16) = v[q].y;
-                    *reinterpret_cast<uint32_t*>(at + q * part_bytes + 32) = v[q].z;
-                    *reinterpret_cast<uint32_t*>(at + q * part_bytes + 48) = v[q].w;
+                for (int i = 0; i < 2 * NK; ++i) {
+                    const int k = k0 + 8 * i;
+                    load8_parts<PB>(M + (int64_t)k * J + jb + j, k < r && j < cols, v[i]);
                 }
-            }
-        } else {
-            for (int i = tid; i < groups * (R / 8); i += 128) {
-                const int j = i / (R / 8), k = i % (R / 8) * 8;
-                uint4 v[PB];
-                load8_parts<PB>(M + (int64_t)(jb + j) * r + k, k < r && j < cols, v);
 #pragma unroll
-                for (int q = 0; q < PB; ++q)
-                    *reinterpret_cast<uint4*>(smem + q * part_bytes + place(j) * pitch + k * 2) = v[q];
+                for (int i = 0; i < 2 * NK; ++i) {
+                    // K rows in the order that puts the four lanes' rows next to one another
+                    const int k = k0 + 8 * i;
+                    uint8_t* at = smem + ((k & ~15) + (k & 3) * 4 + (k >> 2 & 3)) * pitch + place(j) * 2;
+#pragma unroll
+                    for (int q = 0; q < PB; ++q) {
+                        *reinterpret_cast<uint2*>(at + q * part_bytes) = make_uint2(v[i][q].x, v[i][q].z);
+                        *reinterpret_cast<uint2*>(at + q * part_bytes + 16) = make_uint2(v[i][q].y, v[i][q].w);
+                    }
+                }
+            } else {
+                const int k = tid % (2 * NK) * 8, j0 = c + tid / (2 * NK);
+#pragma unroll
+                for (int i = 0; i < 2 * NK; ++i) {
+                    const int j = j0 + i * (64 / NK);
+                    load8_parts<PB>(M + (int64_t)(jb + j) * r + k, k < r && j < cols, v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * NK; ++i)
+#pragma unroll
+                    for (int q = 0; q < PB; ++q)
+                        *reinterpret_cast<uint4*>(smem + q * part_bytes + place(j0 + i * (64 / NK)) * pitch + k * 2) = v[i][q];
             }
         }
     }
+    // rows g and g + 8 of the warp; one past the tile reads the tile's first and writes nothing
+    const float* base[2];
     int64_t at[2];
     bool have[2];
     uint32_t u[PF][NK][4];
@@ -555,7 +570,8 @@ __global__ void __launch_bounds__(128, Parts<T>::f32 * NK <= 8 ? 4 : 2) adapter_
     for (int i = 0; i < 2; ++i) {
         const int q = warp * 16 + g + 8 * i;
         have[i] = q < tile.rows;
-        at[i] = (have[i] ? (int64_t)a.p.perm[tile.pos + q] : 0) * J + jb + 8 * t;
+        at[i] = (int64_t)a.p.perm[tile.pos + (have[i] ? q : 0)] * J + jb + 4 * t;
+        base[i] = a.base + at[i];
 #pragma unroll
         for (int j = 0; j < PF; ++j)
 #pragma unroll
@@ -569,22 +585,16 @@ __global__ void __launch_bounds__(128, Parts<T>::f32 * NK <= 8 ? 4 : 2) adapter_
                 u[j][s][2 + i] = v.y;
             }
     }
-    // what 32 columns from n0 on are added to: 8 of two rows
+    const int lim = cols - 4 * t;
+    const bool based = a.base != nullptr;
+    // what 32 columns from n0 on are added to: 4 and 4 of two rows
     auto fetch = [&](int n0, float4 (&v)[2][2]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 v[i][h] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (!have[i] || n0 + 8 * t >= cols) continue;
-                if (a.base) v[i][h] = *reinterpret_cast<const float4*>(a.base + at[i] + n0 + 4 * h);
-                if (a.add_out) {
-                    const float4 w = *reinterpret_cast<const float4*>(a.out + at[i] + n0 + 4 * h);
-                    v[i][h].x += w.x;
-                    v[i][h].y += w.y;
-                    v[i][h].z += w.z;
-                    v[i][h].w += w.w;
-                }
+                if (based && n0 + 16 * h < lim) v[i][h] = *reinterpret_cast<const float4*>(base[i] + n0 + 16 * h);
             }
     };
     float4 next[2][2][2];  // the next two steps'
@@ -646,18 +656,20 @@ __global__ void __launch_bounds__(128, Parts<T>::f32 * NK <= 8 ? 4 : 2) adapter_
                     }
             }
         }
-        // tile n has columns 2 n, 2 n + 1 of this lane's 8
-        if (n0 + 8 * t < cols) {
+        // tiles 2 h and 2 h + 1 have the pairs of this lane's four columns at 16 h
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!have[i]) continue;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<float4*>(a.out + at[i] + n0 + 4 * h) =
-                        make_float4(add[i][h].x + acc[2 * h][2 * i], add[i][h].y + acc[2 * h][2 * i + 1],
-                                    add[i][h].z + acc[2 * h + 1][2 * i], add[i][h].w + acc[2 * h + 1][2 * i + 1]);
+            for (int h = 0; h < 2; ++h) {
+                if (!have[i] || n0 + 16 * h >= lim) continue;
+                float4 v = make_float4(add[i][h].x + acc[2 * h][2 * i], add[i][h].y + acc[2 * h][2 * i + 1],
+                                       add[i][h].z + acc[2 * h + 1][2 * i], add[i][h].w + acc[2 * h + 1][2 * i + 1]);
+                if (a.base2) {
+                    const float4 w = *reinterpret_cast<const float4*>(a.base2 + at[i] + n0 + 16 * h);
+                    v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+                }
+                *reinterpret_cast<float4*>(a.out + at[i] + n0 + 16 * h) = v;
             }
-        }
     }
 }
 
@@ -721,7 +733,7 @@ __device__ __forceinline__ void pair_parts(const Raw4<__nv_bfloat16>& a, const R
 }
 
 template <typename T, typename TZ, bool TRANS, int MT>
-__global__ void __launch_bounds__(128) adapter_grad_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(const __grid_constant__ GradArgs a) {
     constexpr int PZ = act_parts<TZ, T>(), PF = Parts<T>::f32;
     constexpr int kInPitch = MT * 32 + 16, kInPart = kGradRows * kInPitch, kStage = grad_stage<PF, MT>();
     constexpr int STEPS = kGradRows / 16;
@@ -1034,12 +1046,12 @@ int64_t tile_bound(const moe_adapter_params& p) {
     return p.N / kRows + std::min<int64_t>(p.n_adapters + 1, p.N);
 }
 
-// K slices of a shrink: enough CTAs for two waves of the likely tiles, at least two stages of K each
+// K slices of a shrink: as many CTAs as fit on the GPU at once (two on an SM)
+// for the likely tiles, at least two stages of K each
 int shrink_slices(const moe_adapter_params& p, int K) {
     const int64_t tiles = p.N / kRows + (std::min<int64_t>(p.n_adapters, p.N) + 1) / 2;
-    const int64_t want = (4 * (int64_t)num_sms() + tiles - 1) / std::max<int64_t>(tiles, 1);
     int s = 1;
-    while (s * 2 <= kMaxSlices && s * 2 <= want && K / (s * 2) >= 2 * kShrinkK) s *= 2;
+    while (s * 2 <= kMaxSlices && s * 2 * tiles <= 2 * num_sms() && K / (s * 2) >= 2 * kShrinkK) s *= 2;
     return s;
 }
 
@@ -1071,7 +1083,7 @@ Layout layout_of(const moe_adapter_params& p, bool with_W, bool backward) {
     L.counters = take(CNT_COUNT * 8);
     L.perm = take(N * 4);
     L.seg = take(((size_t)p.n_adapters + 2) * 4);
-    L.one_group = take(5 * 4);  // and the number of tiles
+    L.one_group = take(7 * 4);  // and the number of tiles
     L.tiles = take((size_t)tile_bound(p) * sizeof(Tile));
     // u as parts, or (a few tokens) as partial sums
     L.u = take(std::max(N * r * 2 * parts, N <= kFewN ? 16 * N * r * 4 : 0));
@@ -1097,7 +1109,7 @@ Plan plan_of(const Layout& L, char* ws) {
     p.perm = reinterpret_cast<int32_t*>(ws + L.perm);
     p.seg = reinterpret_cast<int32_t*>(ws + L.seg);
     p.one_group = reinterpret_cast<int32_t*>(ws + L.one_group);
-    p.n_tiles = p.one_group + 4;
+    p.n_tiles = p.one_group + 6;
     p.tiles = reinterpret_cast<Tile*>(ws + L.tiles);
     return p;
 }
@@ -1178,9 +1190,9 @@ cudaError_t launch_expand(const moe_adapter_params& p, const __nv_bfloat16* in, 
     ExpandArgs a{};
     a.in = in;
     a.M = M;
-    a.base = base;
+    a.base = add_out ? out : base;
+    a.base2 = add_out ? base : nullptr;
     a.out = out;
-    a.add_out = add_out;
     a.J = J;
     a.r = p.r;
     a.n_adapters = p.n_adapters;
@@ -1253,7 +1265,19 @@ cudaError_t forward(const moe_adapter_params& p, const T* x, const T* W, const T
     if (e != cudaSuccess) return e;
     if (W) {
         int status = MOE_OK;
-        if (sizeof(T) == 2) e = launch_tc_dense(p.N, p.d_out, p.d_in, x, W, y, plan.counters, st, &status);
+        moe_params q{};  // the projection as a layer of one expert with these rows
+        q.N = p.N;
+        q.d = p.d_out;
+        q.d_f = p.d_in;
+        q.E_r = 1;
+        q.k = 1;
+        q.dtype = p.dtype;
+        if (sizeof(T) == 2 && !few && tc_tile_rows(q) == 256) {
+            // enough rows for CTA pairs: 4096 x 4096 x 4096 in XX us instead of 114 by single CTAs
+            const ExpertWeights E{nullptr, nullptr, W, nullptr, nullptr, nullptr};
+            e = launch_tc_down(q, DOWN_STORE, p.N, x, nullptr, plan.one_group, plan.one_group + 4, E, nullptr, nullptr,
+                               nullptr, y, plan.counters, st, &status);
+        } else if (sizeof(T) == 2) e = launch_tc_dense(p.N, p.d_out, p.d_in, x, W, y, plan.counters, st, &status);
         else
             e = launch_simt_dense(p.N, p.d_out, p.d_in, reinterpret_cast<const float*>(x), p.d_in, 1,
                                   reinterpret_cast<const float*>(W), p.d_in, 1, y, p.d_out, st);
