@@ -242,41 +242,39 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object on the way
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
-class _on_device_of:
-    """The CUDA device of the tensors, made current for one call (the library
-    launches on the current device and, without a stream, on its current
-    stream); tensors of several devices are refused."""
-
-    __slots__ = ("index", "guard")
-
-    def __init__(self, *tensors):
-        self.index, self.guard = -1, None
-        for t in tensors:
-            if t is not None and not isinstance(t, int):
-                i = t.get_device()
-                if i != self.index:
-                    if i < 0:
-                        raise ValueError("libmoe takes device tensors; got a host tensor")
-                    if self.index >= 0:
-                        raise ValueError("libmoe takes tensors of one device; got devices %d and %d" % (self.index, i))
-                    self.index = i
-
-    def __enter__(self):
-        if self.index >= 0:
-            import torch
-            if torch.cuda.current_device() != self.index:
-                self.guard = torch.cuda.device(self.index)
-                self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _enqueue(name: str, params, tensors, stream):
+    """Calls library function `name` (params, the tensors' addresses, stream)
+    with the tensors' device current: the library launches on the current
+    device and, without a stream, on its current stream.  Host tensors and
+    tensors of several devices are refused.  Returns the status."""
+    import torch
+    index, ptrs = -1, []
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            ptrs.append(t)
+            continue
+        i = t.get_device()
+        if i < 0:
+            raise ValueError("libmoe takes device tensors; got a host tensor")
+        if i != index:
+            if index >= 0:
+                raise ValueError(f"libmoe takes tensors of one device; got devices {index} and {i}")
+            index = i
+        if not t.is_contiguous():
+            raise ValueError("libmoe takes contiguous tensors")
+        ptrs.append(t.data_ptr())
+    fn = getattr(lib(), name)
+    if index >= 0 and index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return fn(ctypes.byref(params), *ptrs, _stream(stream))
+    return fn(ctypes.byref(params), *ptrs, _stream(stream))
 
 
 def _check(status: int, where: str):
@@ -354,10 +352,8 @@ def moe_few_workspace_size(p: Params) -> int:
 def moe_forward_few(p, x, W_r, b_r, lat, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, Y, ws, stream=None):
     """moe_forward for at most 32 tokens in two launches; ws of
     moe_few_workspace_size bytes (see moe_forward_few in include/moe.h)."""
-    with _on_device_of(x, W_r, b_r, lat, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, Y, ws):
-        _check(lib().moe_forward_few(ctypes.byref(p), _ptr(x), _ptr(W_r), _ptr(b_r), _ptr(lat), _ptr(W_g),
-                                     _ptr(W_u), _ptr(W_d), _ptr(Ws_g), _ptr(Ws_u), _ptr(Ws_d), _ptr(Y),
-                                     _ptr(ws), _stream(stream)), "moe_forward_few")
+    _check(_enqueue("moe_forward_few", p, (x, W_r, b_r, lat, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, Y, ws), stream),
+           "moe_forward_few")
 
 
 def moe_forward_begin(p, x, W_r, b_r, lat, counts, ws, stream=None):
@@ -566,7 +562,7 @@ def moe_adapter_backward_workspace_size(ap: AdapterParams, with_W: bool = False)
 
 def _typed(what, t, dtype, shape):
     """Refuses a tensor of another type or shape than the call's."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
@@ -591,9 +587,7 @@ def moe_adapter_forward(ap, x, W, A, B, scale, ids, base, y, ws, stream=None):
     for what, t in (("base", base), ("y", y)):
         if t is not None:
             _typed(what, t, f32, (ap.N, ap.d_out))
-    with _on_device_of(x, W, A, B, scale, ids, base, y, ws):
-        _check(lib().moe_adapter_forward(ctypes.byref(ap), _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(scale), _ptr(ids),
-                                         _ptr(base), _ptr(y), _ptr(ws), _stream(stream)), "moe_adapter_forward")
+    _check(_enqueue("moe_adapter_forward", ap, (x, W, A, B, scale, ids, base, y, ws), stream), "moe_adapter_forward")
 
 
 def moe_adapter_backward(ap, x, W, A, B, scale, ids, dy, dx_base, dx, dA, dB, ws, stream=None):
@@ -607,17 +601,14 @@ def moe_adapter_backward(ap, x, W, A, B, scale, ids, dy, dx_base, dx, dA, dB, ws
             _typed(what, t, f32, (ap.N, ap.d_in))
     _typed("dA", dA, f32, (ap.n_adapters, ap.r, ap.d_in))
     _typed("dB", dB, f32, (ap.n_adapters, ap.d_out, ap.r))
-    with _on_device_of(x, W, A, B, scale, ids, dy, dx_base, dx, dA, dB, ws):
-        _check(lib().moe_adapter_backward(ctypes.byref(ap), _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(scale),
-                                          _ptr(ids), _ptr(dy), _ptr(dx_base), _ptr(dx), _ptr(dA), _ptr(dB),
-                                          _ptr(ws), _stream(stream)), "moe_adapter_backward")
+    _check(_enqueue("moe_adapter_backward", ap, (x, W, A, B, scale, ids, dy, dx_base, dx, dA, dB, ws), stream),
+           "moe_adapter_backward")
 
 
 def moe_adapter_check(ap, ws, stream=None) -> int:
     """Waits for the stream; MOE_ERR_INVALID_ARG if the last adapter call on ws
     met an id out of range, MOE_ERR_TIMEOUT, or MOE_OK."""
-    with _on_device_of(ws):
-        return lib().moe_adapter_check(ctypes.byref(ap), _ptr(ws), _stream(stream))
+    return _enqueue("moe_adapter_check", ap, (ws,), stream)
 
 
 def _dropout_types(dp, wide, narrow, step):
@@ -636,15 +627,11 @@ def moe_dropout_forward(dp, Y, residual, out, step=None, stream=None):
     residual may be None; step: a device tensor of one int64 that is added to
     the offset when the kernel runs."""
     _dropout_types(dp, ("Y", Y), (("residual", residual), ("out", out)), step)
-    with _on_device_of(Y, residual, out, step):
-        _check(lib().moe_dropout_forward(ctypes.byref(dp), _ptr(Y), _ptr(residual), _ptr(out), _ptr(step),
-                                         _stream(stream)), "moe_dropout_forward")
+    _check(_enqueue("moe_dropout_forward", dp, (Y, residual, out, step), stream), "moe_dropout_forward")
 
 
 def moe_dropout_backward(dp, dout, dY, step=None, stream=None):
     """dY = the gradient of the layer's output for the gradient dout of
     moe_dropout_forward's out, under the same params and step."""
     _dropout_types(dp, ("dY", dY), (("dout", dout),), step)
-    with _on_device_of(dout, dY, step):
-        _check(lib().moe_dropout_backward(ctypes.byref(dp), _ptr(dout), _ptr(dY), _ptr(step), _stream(stream)),
-               "moe_dropout_backward")
+    _check(_enqueue("moe_dropout_backward", dp, (dout, dY, step), stream), "moe_dropout_backward")
