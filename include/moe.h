@@ -352,7 +352,7 @@ MOE_API moe_status moe_forward(const moe_params* p, const void* x, const void* W
  *   - ws is of moe_few_workspace_size bytes; its first part is laid out as
  *     moe_workspace_layout says (x_perm, h, h_shared and the rerouting
  *     candidates are not written, so moe_backward cannot follow);
- *   - bf16 layers keep h to 16 mantissa bits instead of rounding it to bf16;
+ *   - bf16 layers keep h to 24 mantissa bits instead of rounding it to bf16;
  *   - Y does not depend on the order of any atomics: the same inputs give the
  *     same bits;
  *   - the capacity limit and the overflow policies MOE_REJECT_ZERO and
@@ -653,10 +653,9 @@ MOE_API moe_status moe_backward_check(const moe_params* p, const void* bws, moe_
  *   fp32, overwritten (adapters without tokens get zeros).
  * It needs nothing of the forward call.
  *
- * Precision: fp32 accumulation.  16-bit operands are used as they are; fp32
- * operands of bf16 calls (u, v, dy) as two bf16 parts (16 mantissa bits), of
- * fp32 calls as three (24 bits), except the fp32 projection, which runs on the
- * CUDA cores.  Same inputs give the same bits without W; with W the projection
+ * Precision: fp32 accumulation.  16-bit operands are used as they are, fp32 ones
+ * (u, v, dy; all of an fp32 call's) to 24 mantissa bits, except that W^T dy of a
+ * bf16 call takes dy to 16 bits; the fp32 projection runs on the CUDA cores.  Same inputs give the same bits without W; with W the projection
  * may split K over CTAs (fp32 additions in any order).
  * Constraints: d_in, d_out and r multiples of 8, r <= 128, n_adapters <= 1024,
  * d_in and d_out <= 2^23, N < 2^30 (fp32 with W: N <= 65535 * 64); else MOE_ERR_UNSUPPORTED.  Pointers

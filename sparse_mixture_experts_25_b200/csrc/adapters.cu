@@ -20,9 +20,10 @@
 // and nothing is summed by atomics: results do not depend on the schedule.
 //
 // Arithmetic: mma.sync m16n8k16 on bf16 parts, fp32 accumulation.  A 16-bit
-// operand is one part; a 32-bit one is the sum of bf16 parts, two (16 bits)
-// beside 16-bit adapters and three (24 bits) in fp32, where the products of
-// parts up to 2^-16 of the first are kept.  (tcgen05 tiles of 64 or 128 rows
+// operand is one part; a 32-bit one is the sum of three bf16 parts (24 bits), and
+// where two of them meet the products of parts up to 2^-16 of the first are kept
+// (six of nine).  With two parts (16 bits) the results were 2.5e-6 to 4.6e-6 of
+// their norm off.  (tcgen05 tiles of 64 or 128 rows
 // would be mostly padding at these ranks: the tensor pipe is not what bounds.)
 // u and v are stored as such parts, in the sorted order.  The tensor pipe
 // truncates its running sums: left to run over K = 1000 in fp32, y was off by
@@ -49,19 +50,20 @@ namespace {
 
 constexpr int kRows = 64;          // rows of a tile
 constexpr int kShrinkK = 64;       // K elements of a shrink stage
-constexpr int kStages = 4;         // stages of the shrink's and the grad's rings
+constexpr int kStages = 4;         // stages of the shrink's ring
+constexpr int kGradStages = 3;     // of the grad's: room for three CTAs on an SM up to rank 64
 constexpr int kGradCols = 128;     // columns of a grad CTA
 constexpr int kGradRows = 32;      // tokens of a grad stage
 constexpr int kGradFlush = 4;      // grad stages between additions to the sums
 constexpr int kFewN = 32;          // batches of the few-token form
 constexpr int kMaxSlices = 8;      // K slices of a shrink (CTAs of a cluster)
 
-// bf16 parts of an operand: of type T itself, and of an fp32 one beside T
+// bf16 parts of an operand: of type T itself, and of an fp32 one
 template <typename T>
 struct Parts;
 template <>
 struct Parts<__nv_bfloat16> {
-    static constexpr int self = 1, f32 = 2;
+    static constexpr int self = 1, f32 = 3;
 };
 template <>
 struct Parts<float> {
@@ -507,7 +509,7 @@ __host__ __device__ constexpr int expand_part(int span) {
 
 // as many CTAs on an SM as the parts of u leave registers for
 template <typename T, bool NN, int NK>
-__global__ void __launch_bounds__(128, Parts<T>::f32 * NK <= 4 ? 4 : Parts<T>::f32 * NK <= 8 ? 3 : 2) adapter_expand_kernel(const __grid_constant__ ExpandArgs a) {
+__global__ void __launch_bounds__(128, NK == 1 ? 4 : NK <= 4 ? 3 : 2) adapter_expand_kernel(const __grid_constant__ ExpandArgs a) {
     constexpr int PB = Parts<T>::self, PF = Parts<T>::f32;
     constexpr int R = NK * 16;
     const int pitch = NN ? a.span * 2 + 16 : expand_pitch(R), part_bytes = expand_part<T, NN, NK>(a.span);
@@ -702,7 +704,7 @@ struct GradArgs {
 template <int PF, int MT>
 constexpr int grad_stage() { return PF * kGradRows * (MT * 32 + 16) + kGradRows * 4; }
 template <int PF, int MT>
-constexpr size_t grad_smem() { return (size_t)kStages * grad_stage<PF, MT>() + (size_t)MT * 16 * 128 * 4; }
+constexpr size_t grad_smem() { return (size_t)kGradStages * grad_stage<PF, MT>() + (size_t)MT * 16 * 128 * 4; }
 
 // 4 consecutive elements as they are in memory
 template <typename TZ>
@@ -738,7 +740,7 @@ __global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(cons
     constexpr int kInPitch = MT * 32 + 16, kInPart = kGradRows * kInPitch, kStage = grad_stage<PF, MT>();
     constexpr int STEPS = kGradRows / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    float* sums = reinterpret_cast<float*>(smem + kStages * kStage);  // [MT * 16][128 threads]
+    float* sums = reinterpret_cast<float*>(smem + kGradStages * kStage);  // [MT * 16][128 threads]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int r = a.r, J = a.J;
     const int tokens = a.p.seg[a.n_adapters];  // those that have an adapter
@@ -763,7 +765,7 @@ __global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(cons
         const int seg1 = min(seg_end, hi), c0 = 0, c1 = (seg1 - beg + kGradRows - 1) / kGradRows;
         auto fill = [&](int c) {
             if (c < c1) {
-                const uint32_t st = smem_addr(smem) + c % kStages * kStage;
+                const uint32_t st = smem_addr(smem) + c % kGradStages * kStage;
                 const int pos = beg + c * kGradRows;
 #pragma unroll
                 for (int i = 0; i < IN; ++i) {
@@ -784,7 +786,7 @@ __global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(cons
         };
         // rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of each step of 16 tokens
         auto fetch = [&](int c, Raw4<TZ> (&z)[STEPS][4]) {
-            const int32_t* tok = reinterpret_cast<const int32_t*>(smem + c % kStages * kStage + PF * kInPart);
+            const int32_t* tok = reinterpret_cast<const int32_t*>(smem + c % kGradStages * kStage + PF * kInPart);
 #pragma unroll
             for (int s = 0; s < STEPS; ++s)
 #pragma unroll
@@ -795,7 +797,7 @@ __global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(cons
                 }
         };
 #pragma unroll
-        for (int c = 0; c < kStages - 1; ++c) fill(c0 + c);
+        for (int c = 0; c < kGradStages - 1; ++c) fill(c0 + c);
         float acc[MT][4][4] = {};
         auto flush = [&](bool first, bool last) {
 #pragma unroll
@@ -810,18 +812,18 @@ __global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(cons
         };
         Raw4<TZ> z[STEPS][4];
         if (c0 < c1) {
-            copies_wait<kStages - 2>();
+            copies_wait<kGradStages - 2>();
             __syncthreads();
             fetch(c0, z);
         }
         bool first = true;
         for (int c = c0; c < c1; ++c) {
-            copies_wait<kStages - 3>();  // this stage and the next
+            copies_wait<kGradStages - 3>();  // this stage and the next
             __syncthreads();
-            fill(c + kStages - 1);
+            fill(c + kGradStages - 1);
             Raw4<TZ> ahead[STEPS][4];
             if (c + 1 < c1) fetch(c + 1, ahead);
-            const uint8_t* st = smem + c % kStages * kStage;
+            const uint8_t* st = smem + c % kGradStages * kStage;
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int m = lane >> 3, i = lane & 7;

@@ -34,9 +34,10 @@
 // a tcgen05 tile (M = 64 or 128 rows) would fix the cut at that many rows and
 // leave SMs without work.  A lane reads 8 consecutive K elements of its row
 // (16 bytes) and feeds them to two MMAs; both operands use the same order of K,
-// so the sum is unchanged.  h is kept as bf16 hi + lo parts (16 mantissa bits,
-// relative error 6e-7 rms): rounding it to one bf16 would be the layer's
-// largest error, and the second part costs one more MMA on a 1/3 of the bytes.
+// so the sum is unchanged.  h is kept as three bf16 parts (24 mantissa bits):
+// rounding it to one bf16 would be the layer's largest error by far, two parts
+// still left Y 2.5e-6 of its norm off, and the third costs one more MMA on a
+// third of the bytes.
 // fp32: FFMA, one warp per two rows, nothing rounded.
 //
 // No atomics are used on the outputs: results do not depend on the schedule.
@@ -72,7 +73,7 @@ struct FewArgs {
     int reject;              // moe_reject_policy (zero or renorm)
     int C;                   // requests an expert takes, at most N
     long long C_stat;        // the capacity as the statistics report it
-    void* h;                 // bf16: hi plane, lo plane; fp32: one plane.  [N k + N][ldh]
+    void* h;                 // bf16: three planes of parts; fp32: one plane.  [N k + N][ldh]
     int64_t h_plane;
     int ldh;
     float* Y;
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     constexpr int ST = few_stages(NT);
     constexpr int SB = few_stage_bytes(NT);
     constexpr int ES = BF16 ? 2 : 4;
-    constexpr int PL = BF16 ? 2 : 1;  // parts that h is kept in
+    constexpr int PL = BF16 ? 3 : 1;  // parts that h is kept in
     static_assert(SB / (kFewRows + PL * NT * 8) >= 128 + 64, "a stage holds a piece of every row");
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     if (warp >= kFewConsumers) {
         // ---- producers: row i of a stage is copied by lane i / 4 of warp i % 4 ----
         const int mine = lane * kFewProducers + warp - kFewConsumers;
-        static_assert(kFewRows + 2 * kFewMaxTokens <= 32 * kFewProducers, "a lane for every row of a stage");
+        static_assert(kFewRows + 3 * kFewMaxTokens <= 32 * kFewProducers, "a lane for every row of a stage");
         RingPos pos;
         int used = 0;  // stages filled at least once
         // takes the next stage, which this warp copies `rows` pieces of `bytes` to
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                               ((int64_t)gr.e * a.d + c + mine) * gr.F * ES;
                         slot = mine;
                     } else if (mine < total) {
-                        const int r = mine - nc, pl = r >= gr.R ? 1 : 0;
+                        const int r = mine - nc, pl = r >= 2 * gr.R ? 2 : r >= gr.R ? 1 : 0;
                         src = static_cast<const uint8_t*>(a.h) +
                               ((int64_t)pl * a.h_plane + (int64_t)(gr.row0 + r - pl * gr.R) * a.ldh) * ES;
                         slot = kFewRows + r;
@@ -676,8 +677,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                             if (M == 1 || n * 8 < R) {
                                 const int r = n * 8 + g;
                                 mma_step(acc[0][n], acc[1][n], lo, hi, ld(kFewRows + r, r < R));
-                                if (decltype(planes)::value > 1)
+                                if (decltype(planes)::value > 1) {
+                                    mma_step(acc[2][n], acc[3][n], lo, hi, ld(kFewRows + 2 * R + r, r < R));
                                     mma_step(acc[2][n], acc[3][n], lo, hi, ld(kFewRows + R + r, r < R));
+                                }
                             }
                         }
                     }
@@ -729,7 +732,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             else f(std::integral_constant<int, NT>{});
         };
         const std::integral_constant<int, 1> x_parts{};
-        const std::integral_constant<int, 2> h_parts{};
+        const std::integral_constant<int, PL> h_parts{};
 
         // gate/up: h of this CTA's hidden units
         int tile = 0, nj;
@@ -760,13 +763,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                         zg += p[q * (NT * 128)];
                         zu += p[q * (NT * 128) + 64];
                     }
-                    const float hv = zg / (1.0f + expf(-zg)) * zu;
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(hv);
+                    float hv = zg / (1.0f + expf(-zg)) * zu;
                     __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.h) + (int64_t)(row0 + r) * a.ldh + j + unit;
-                    h[0] = hi;
-                    // an infinite h has no second part
-                    const float rest = hv - __bfloat162float(hi);
-                    h[a.h_plane] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+#pragma unroll
+                    for (int q = 0; q < PL; ++q) {
+                        const __nv_bfloat16 part = __float2bfloat16_rn(hv);
+                        h[q * a.h_plane] = part;
+                        hv -= __bfloat162float(part);
+                        hv = isfinite(hv) ? hv : 0.f;  // one that is not finite is its first part
+                    }
                 }
             } else {
                 float acc[2][NT * 8] = {};
@@ -912,7 +917,7 @@ FewLayout few_layout(const moe_params& p, size_t after) {
     L.part = L.bar + 256;
     L.h = L.part + up((size_t)few_score_slices(p.d, p.E_r) * p.N * p.E_r * 4);
     const size_t rows = (size_t)p.N * p.k + (p.d_f_shared > 0 ? (size_t)p.N : 0);
-    L.total = L.h + up(rows * (size_t)std::max(p.d_f, p.d_f_shared) * 4);
+    L.total = L.h + up(rows * (size_t)std::max(p.d_f, p.d_f_shared) * (p.dtype == MOE_BF16 ? 3 * 2 : 4));
     return L;
 }
 

@@ -4,10 +4,10 @@ bits, element by element.
 Bounds, with e = 2^-23 for a rounded or truncated addition:
   * a sum of n products is off by at most n e times the sum of the products'
     magnitudes;
-  * an operand held as two bf16 parts is off by at most 2^-16 of its value (a
-    half step is 2^-8, twice), as three by 2^-24; the products of parts that
-    are left out are below 2^-16 (two by two parts) and 2^-22 (three by three)
-    of the whole;
+  * an operand held as three bf16 parts is off by at most 2^-24 of its value (a
+    half step is 2^-8, three times); the products of parts that are left out
+    (second by third and beyond) are below 2^-22 of the whole.  The dy of a
+    bf16 projection is held as two parts: 2^-16;
   * an error in u or v carries on through the magnitudes of what multiplies it.
 """
 import ctypes
@@ -61,8 +61,8 @@ def reference(t, bf16):
     f = {n: (v.double() if v is not None and n != "ids" else v) for n, v in t.items()}
     N, d_in = t["x"].shape
     d_out, a = t["B"].shape[1], t["A"].shape[0]
-    part = 2.0 ** -16 if bf16 else 2.0 ** -21  # an fp32 operand's parts, or both and the products left out
-    both = 3 * 2.0 ** -16 if bf16 else 2.0 ** -21
+    part = 2.0 ** -21  # fp32 operands' parts and the products left out
+    split = 2.0 ** -16 if bf16 else 0.0  # dy in front of W
     out = {"y": torch.zeros(N, d_out, dtype=torch.float64), "dx": torch.zeros(N, d_in, dtype=torch.float64),
            "dA": torch.zeros_like(f["A"]), "dB": torch.zeros_like(f["B"])}
     tol = {n: torch.zeros_like(v) for n, v in out.items()}
@@ -74,7 +74,7 @@ def reference(t, bf16):
         out["y"] += f["x"] @ f["W"].T
         tol["y"] += (d_in + 2) * E * (f["x"].abs() @ f["W"].abs().T)
         out["dx"] += f["dy"] @ f["W"]
-        tol["dx"] += ((2 * d_out + 2) * E + part) * (f["dy"].abs() @ f["W"].abs())
+        tol["dx"] += ((2 * d_out + 2) * E + split) * (f["dy"].abs() @ f["W"].abs())
     for i in range(a):
         at = torch.nonzero(t["ids"] == i).reshape(-1)
         if not len(at):
@@ -82,16 +82,16 @@ def reference(t, bf16):
         A, B, s, x, dy = f["A"][i], f["B"][i], f["scale"][i], f["x"][at], f["dy"][at]
         r, n = A.shape[0], len(at)
         u, v = s * (x @ A.T), s * (dy @ B)
-        eu = s * ((d_in + 4) * E + (0 if bf16 else part)) * (x.abs() @ A.abs().T) + part * u.abs()
-        ev = s * ((2 * d_out + 4) * E + part) * (dy.abs() @ B.abs()) + part * v.abs()
+        eu = s * (((1 if bf16 else 6) * d_in + 4) * E + (0 if bf16 else part)) * (x.abs() @ A.abs().T) + part * u.abs()
+        ev = s * ((6 * d_out + 4) * E + part) * (dy.abs() @ B.abs()) + part * v.abs()
         out["y"][at] += u @ B.T
-        tol["y"][at] += eu @ B.abs().T + ((2 * r + 3) * E + part) * (u.abs() @ B.abs().T)
+        tol["y"][at] += eu @ B.abs().T + ((6 * r + 3) * E + part) * (u.abs() @ B.abs().T)
         out["dx"][at] += v @ A
-        tol["dx"][at] += ev @ A.abs() + ((2 * r + 3) * E + part) * (v.abs() @ A.abs())
+        tol["dx"][at] += ev @ A.abs() + ((6 * r + 3) * E + part) * (v.abs() @ A.abs())
         out["dA"][i] = v.T @ x
-        tol["dA"][i] = ev.T @ x.abs() + ((2 * n + 2) * E + part) * (v.abs().T @ x.abs())
+        tol["dA"][i] = ev.T @ x.abs() + ((6 * n + 2) * E + part) * (v.abs().T @ x.abs())
         out["dB"][i] = dy.T @ u
-        tol["dB"][i] = dy.abs().T @ eu + ((3 * n + 2) * E + both) * (dy.abs().T @ u.abs())
+        tol["dB"][i] = dy.abs().T @ eu + ((6 * n + 2) * E + part) * (dy.abs().T @ u.abs())
     return out, tol
 
 

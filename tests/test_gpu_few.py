@@ -9,8 +9,8 @@ on the GPU's routing records, within a bound that follows the arithmetic:
     addition; 2^-23 also covers one that truncates);
   * SiLU moves by at most 1.1 times its argument's error, and its own fp32
     evaluation is off by a few 2^-24 (bounded by 2^-20 of its value);
-  * bf16 layers hold h as two bf16 parts: a half step of the second is at most
-    2^-8 times 2^-8 of h.
+  * bf16 layers hold h as three bf16 parts: a half step of the third is at most
+    2^-24 of h.
 """
 import numpy as np
 import pytest
@@ -85,7 +85,7 @@ def layer64(w, dev, rec):
         ez, eu = (w.d * step * (x.abs() @ m.abs().T) for m in (Wg, Wu))
         silu = z * torch.sigmoid(z)
         h = silu * u
-        eh = 1.1 * ez * (u.abs() + eu) + silu.abs() * eu + (2.0 ** -20 + (2.0 ** -16 if w.dtype else 0.0)) * h.abs()
+        eh = 1.1 * ez * (u.abs() + eu) + silu.abs() * eu + (2.0 ** -20 + 2.0 ** -24) * h.abs()
         K = Wd.shape[1]
         y, mag = h @ Wd.T, h.abs() @ Wd.abs().T
         ey = eh @ Wd.abs().T + K * step * mag
