@@ -30,9 +30,12 @@
 // 4.9e-6 of its norm.  So a long sum is kept outside: the products of one stage
 // are summed from zero (small parts first) and added to it with rounding.
 //
-// A few tokens (N <= 32) take another form: no sort, one CTA per token and
-// slice of K, then one thread per output; two launches instead of three, and no
-// row of a tile is wasted on a token with an adapter of its own.
+// Few tokens take another form (see takes_tokens): no sort, one CTA per token
+// and slice of K, then one thread per output; two launches instead of three, and
+// no row of a tile is wasted on a token with an adapter of its own.
+//
+// The kernels of a call are set up while the one before runs and wait for it
+// themselves (programmatic launches), which saves about half a microsecond each.
 //
 // W runs on the layer's own GEMMs (tcgen05 for bf16, dy as two bf16 parts).
 #include "moe_internal.cuh"
@@ -55,7 +58,6 @@ constexpr int kGradStages = 3;     // of the grad's: room for three CTAs on an S
 constexpr int kGradCols = 128;     // columns of a grad CTA
 constexpr int kGradRows = 32;      // tokens of a grad stage
 constexpr int kGradFlush = 4;      // grad stages between additions to the sums
-constexpr int kFewN = 32;          // batches of the few-token form
 constexpr int kMaxSlices = 8;      // K slices of a shrink (CTAs of a cluster)
 
 // bf16 parts of an operand: of type T itself, and of an fp32 one
@@ -158,6 +160,13 @@ __device__ __forceinline__ void copies_wait() {
 }
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
+// Every kernel here begins with it: the next one of the call may get ready, and
+// what the ones before have written is there from here on.
+__device__ __forceinline__ void in_turn() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // whether the product of parts i and j counts beside operands of PA and PB parts
 template <int PA, int PB>
 __device__ __forceinline__ constexpr bool counts(int i, int j) {
@@ -171,6 +180,7 @@ __device__ __forceinline__ constexpr bool counts(int i, int j) {
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t* ids, int N, int n_adapters, Plan p) {
     extern __shared__ int32_t sm[];
+    in_turn();
     const int nb = n_adapters + 1;
     int32_t* cnt = sm;               // [32][nb] tokens of bucket b before warp w's next one
     int32_t* first = sm + 32 * nb;   // [nb + 1]
@@ -327,6 +337,7 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(const __
     constexpr int kXPitch = shrink_x_pitch<TA>();
     extern __shared__ __align__(128) uint8_t smem[];
     const cg::cluster_group cluster = cg::this_cluster();
+    in_turn();
     if ((int)blockIdx.x >= *a.p.n_tiles) return;  // the same for the whole cluster
     const Tile tile = a.p.tiles[blockIdx.x];
     if (tile.adapter >= a.n_adapters) return;
@@ -404,39 +415,41 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(const __
         fill();
         const uint8_t* xs = smem + c % kStages * stage_bytes;
         const uint8_t* ms = xs + kRows * kXPitch;
-        uint4 x[2][PA];
+        if (row0 < tile.rows) {  // else none of this warp's rows is in the tile
+            uint4 x[2][PA];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            load8_parts<PA>(reinterpret_cast<const TA*>(xs + (row0 + g + 8 * i) * kXPitch) + step * 32 + t * 8, true, x[i]);
+            for (int i = 0; i < 2; ++i)
+                load8_parts<PA>(reinterpret_cast<const TA*>(xs + (row0 + g + 8 * i) * kXPitch) + step * 32 + t * 8, true, x[i]);
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            if (n * 8 >= r) break;
-            uint4 b[PB];
-            if constexpr (!NN) {
-                load8_parts<PB>(reinterpret_cast<const T*>(ms + (n * 8 + g) * m_pitch) + step * 32 + t * 8, true, b);
-            } else if constexpr (sizeof(T) == 2) {
-                const int m = lane >> 3, i = lane & 7;
-                uint32_t v[4];
-                ldmatrix_x4_trans(v, ms + (step * 32 + ((i & 1) + 2 * m) * 4 + (i >> 1)) * m_pitch + n * 16);
-                b[0] = make_uint4(v[0], v[1], v[2], v[3]);
-            } else {
-                float v[8];
+            for (int n = 0; n < NQ; ++n) {
+                if (n * 8 >= r) break;
+                uint4 b[PB];
+                if constexpr (!NN) {
+                    load8_parts<PB>(reinterpret_cast<const T*>(ms + (n * 8 + g) * m_pitch) + step * 32 + t * 8, true, b);
+                } else if constexpr (sizeof(T) == 2) {
+                    const int m = lane >> 3, i = lane & 7;
+                    uint32_t v[4];
+                    ldmatrix_x4_trans(v, ms + (step * 32 + ((i & 1) + 2 * m) * 4 + (i >> 1)) * m_pitch + n * 16);
+                    b[0] = make_uint4(v[0], v[1], v[2], v[3]);
+                } else {
+                    float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = *reinterpret_cast<const float*>(ms + (step * 32 + e * 4 + t) * m_pitch + (n * 8 + g) * 4);
-                split8<PB>(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), b);
-            }
-            // small products first
-#pragma unroll
-            for (int level = (PA > PB ? PA : PB) - 1; level >= 0; --level)
-#pragma unroll
-                for (int j = 0; j < PB; ++j) {
-                    const int i = level - j;
-                    if (i < 0 || i >= PA) continue;
-                    const uint4 &lo = x[0][i], &hi = x[1][i];
-                    mma_bf16(acc[n], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
-                    mma_bf16(acc[n], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = *reinterpret_cast<const float*>(ms + (step * 32 + e * 4 + t) * m_pitch + (n * 8 + g) * 4);
+                    split8<PB>(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), b);
                 }
+                // small products first
+#pragma unroll
+                for (int level = (PA > PB ? PA : PB) - 1; level >= 0; --level)
+#pragma unroll
+                    for (int j = 0; j < PB; ++j) {
+                        const int i = level - j;
+                        if (i < 0 || i >= PA) continue;
+                        const uint4 &lo = x[0][i], &hi = x[1][i];
+                        mma_bf16(acc[n], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
+                        mma_bf16(acc[n], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
+                    }
+            }
         }
         if (c % kShrinkFlush == kShrinkFlush - 1) flush();
     }
@@ -514,6 +527,7 @@ __global__ void __launch_bounds__(128, NK == 1 ? 4 : NK <= 4 ? 3 : 2) adapter_ex
     constexpr int R = NK * 16;
     const int pitch = NN ? a.span * 2 + 16 : expand_pitch(R), part_bytes = expand_part<T, NN, NK>(a.span);
     extern __shared__ __align__(128) uint8_t smem[];
+    in_turn();
     if ((int)blockIdx.x >= *a.p.n_tiles) return;
     const Tile tile = a.p.tiles[blockIdx.x];
     const bool none = tile.adapter >= a.n_adapters;
@@ -603,6 +617,7 @@ __global__ void __launch_bounds__(128, NK == 1 ? 4 : NK <= 4 ? 3 : 2) adapter_ex
     fetch(0, next[0]);
     fetch(32, next[1]);
     __syncthreads();
+    if (warp * 16 >= tile.rows) return;  // none of this warp's rows is in the tile
 #pragma unroll 2
     for (int n0 = 0; n0 < cols; n0 += 32) {
         float4 add[2][2];
@@ -680,7 +695,7 @@ __global__ void __launch_bounds__(128, NK == 1 ? 4 : NK <= 4 ? 3 : 2) adapter_ex
 //   TRANS = false: dA_a [r, J] from v and x;  TRANS = true: dB_a [J, r] from u and dy
 // A CTA has 128 columns and a range of the sorted tokens, the same for every CTA
 // of the row whatever the adapters' shares (cut by adapter instead, the largest
-// one's CTAs ran alone at the end: 143 against XX us for dB of 8192 tokens of
+// one's CTAs ran alone at the end: 143 against 77 us for dB of 8192 tokens of
 // four uneven adapters, r = 64, d = 4096).  An adapter that lies in one range is
 // written to its place; one that continues in others leaves partial sums, at
 // most one per range and adapter met, which the reduction adds in order.  Each
@@ -743,6 +758,7 @@ __global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(cons
     float* sums = reinterpret_cast<float*>(smem + kGradStages * kStage);  // [MT * 16][128 threads]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int r = a.r, J = a.J;
+    in_turn();
     const int tokens = a.p.seg[a.n_adapters];  // those that have an adapter
     const int lo = (int)((int64_t)tokens * blockIdx.y / gridDim.y), hi = (int)((int64_t)tokens * (blockIdx.y + 1) / gridDim.y);
     if (lo >= hi) return;
@@ -893,6 +909,7 @@ __global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(cons
 // without tokens.  CTA (i, a): some of adapter a's elements.
 __global__ void __launch_bounds__(256)
     adapter_reduce_kernel(const float4* part, const int32_t* seg, int n_adapters, int ranges, int64_t n4, float4* out) {
+    in_turn();
     const int adapter = blockIdx.y, seg0 = seg[adapter], seg1 = seg[adapter + 1];
     const int64_t tokens = seg[n_adapters];
     float4* to = out + (int64_t)adapter * n4;
@@ -924,6 +941,7 @@ __global__ void __launch_bounds__(256)
 // dy as two bf16 parts, the operands of W^T dy
 __global__ void __launch_bounds__(256) adapter_split_kernel(const float* v, int64_t n, __nv_bfloat16* hi,
                                                             __nv_bfloat16* lo) {
+    in_turn();
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
         uint4 p[2];
         load8_parts<2>(v + i, true, p);
@@ -1057,6 +1075,18 @@ int shrink_slices(const moe_adapter_params& p, int K) {
     return s;
 }
 
+// Whether a batch takes the form of one CTA per token.  It reads an adapter once
+// for each of its tokens (from L2 mostly), N r (d_in + d_out) elements in all,
+// where the sorted tiles cost about 12 to 30 us however few the tokens; measured
+// at widths of 1024 and 4096 and ranks of 8 to 64 the two meet at 25 to 50 MB in
+// bf16 (32 adapters, d = 4096, r = 16: 64 tokens 7.9 against 17.9 us, 192 tokens
+// 19.8 against 18.6) and at 130 MB and more in fp32 (128 tokens 18.5 against 32.0
+// us, 256 tokens 32.8 against 33.7).
+bool takes_tokens(const moe_adapter_params& p) {
+    const int64_t bytes = p.N * p.r * ((int64_t)p.d_in + p.d_out) * (int64_t)esize(p.dtype);
+    return p.N <= 32 || (p.N <= 256 && bytes <= (p.dtype == MOE_BF16 ? 32 : 128) * (int64_t)(1 << 20));
+}
+
 int few_slices(int64_t N, int K) {
     return (int)std::max<int64_t>(1, std::min<int64_t>({16, 2 * num_sms() / std::max<int64_t>(N, 1), K / 256}));
 }
@@ -1088,7 +1118,7 @@ Layout layout_of(const moe_adapter_params& p, bool with_W, bool backward) {
     L.one_group = take(7 * 4);  // and the number of tiles
     L.tiles = take((size_t)tile_bound(p) * sizeof(Tile));
     // u as parts, or (a few tokens) as partial sums
-    L.u = take(std::max(N * r * 2 * parts, N <= kFewN ? 16 * N * r * 4 : 0));
+    L.u = take(std::max(N * r * 2 * parts, !backward && takes_tokens(p) ? few_slices(p.N, p.d_in) * N * r * 4 : 0));
     if (backward) {
         L.v = take(N * r * 2 * parts);
         if (with_W && p.dtype == MOE_BF16) {
@@ -1116,12 +1146,28 @@ Plan plan_of(const Layout& L, char* ws) {
     return p;
 }
 
+// launches a kernel of a call in turn behind the one before it on the stream
+template <typename... P, typename... Q>
+cudaError_t launch(void (*kern)(P...), dim3 grid, int block, size_t smem, cudaStream_t st, bool behind, Q... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = behind ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, P(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 cudaError_t launch_plan(const moe_adapter_params& p, const int32_t* ids, const Plan& plan, cudaStream_t st) {
     const size_t smem = (size_t)(34 * (p.n_adapters + 2)) * 4;
     cudaError_t e = allow_smem_once<adapter_plan_kernel>(34 * (kMaxAdapters + 2) * 4);
     if (e != cudaSuccess) return e;
-    adapter_plan_kernel<<<1, 1024, smem, st>>>(ids, (int)p.N, p.n_adapters, plan);
-    return cudaGetLastError();
+    return launch(adapter_plan_kernel, dim3(1), 1024, smem, st, false, ids, (int)p.N, p.n_adapters, plan);
 }
 
 template <typename T, typename TA, bool NN, int NQ>
@@ -1139,13 +1185,15 @@ cudaError_t launch_shrink_q(const moe_adapter_params& p, ShrinkArgs a, cudaStrea
     cfg.blockDim = dim3(kShrinkThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 1;
     attr[0].val.clusterDim.y = (unsigned)slices;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, kern, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -1170,7 +1218,7 @@ cudaError_t launch_shrink(const moe_adapter_params& p, const TA* X, const T* M, 
 }
 
 template <typename T, bool NN, int NK>
-cudaError_t launch_expand_k(const moe_adapter_params& p, ExpandArgs a, cudaStream_t st) {
+cudaError_t launch_expand_k(const moe_adapter_params& p, ExpandArgs a, bool behind, cudaStream_t st) {
     constexpr auto kern = adapter_expand_kernel<T, NN, NK>;
     // columns of a CTA: at most what leaves room for five CTAs on an SM, and few
     // enough that there are CTAs for two waves
@@ -1182,8 +1230,7 @@ cudaError_t launch_expand_k(const moe_adapter_params& p, ExpandArgs a, cudaStrea
     cudaError_t e = allow_smem_once<kern>(std::max(smem(128), (size_t)100 * 1024));
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)tile_bound(p), (unsigned)((a.J + a.span - 1) / a.span), 1);
-    kern<<<grid, 128, smem(a.span), st>>>(a);
-    return cudaGetLastError();
+    return launch(kern, grid, 128, smem(a.span), st, behind, a);
 }
 
 template <typename T, bool NN>
@@ -1192,6 +1239,7 @@ cudaError_t launch_expand(const moe_adapter_params& p, const __nv_bfloat16* in, 
     ExpandArgs a{};
     a.in = in;
     a.M = M;
+    // behind a projection, whose kernel does not say when it may be followed, an ordinary launch
     a.base = add_out ? out : base;
     a.base2 = add_out ? base : nullptr;
     a.out = out;
@@ -1200,10 +1248,10 @@ cudaError_t launch_expand(const moe_adapter_params& p, const __nv_bfloat16* in, 
     a.n_adapters = p.n_adapters;
     a.N = p.N;
     a.p = plan;
-    if (p.r <= 16) return launch_expand_k<T, NN, 1>(p, a, st);
-    if (p.r <= 32) return launch_expand_k<T, NN, 2>(p, a, st);
-    if (p.r <= 64) return launch_expand_k<T, NN, 4>(p, a, st);
-    return launch_expand_k<T, NN, 8>(p, a, st);
+    if (p.r <= 16) return launch_expand_k<T, NN, 1>(p, a, !add_out, st);
+    if (p.r <= 32) return launch_expand_k<T, NN, 2>(p, a, !add_out, st);
+    if (p.r <= 64) return launch_expand_k<T, NN, 4>(p, a, !add_out, st);
+    return launch_expand_k<T, NN, 8>(p, a, !add_out, st);
 }
 
 template <typename T, typename TZ, bool TRANS, int MT>
@@ -1213,8 +1261,7 @@ cudaError_t launch_grad_m(const GradArgs& a, dim3 grid, cudaStream_t st) {
     static_assert(smem <= 232448, "shared memory per CTA");
     cudaError_t e = allow_smem_once<kern>(smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, 128, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch(kern, grid, 128, smem, st, true, a);
 }
 
 template <typename T, typename TZ, bool TRANS>
@@ -1240,9 +1287,9 @@ cudaError_t launch_grad(const moe_adapter_params& p, const __nv_bfloat16* in, co
     // a CTA for 1024 of an adapter's elements, fewer where there are many adapters
     const int64_t n4 = (int64_t)p.r * J / 4;
     const int64_t blocks = std::min<int64_t>((n4 + 255) / 256, std::max<int64_t>(1, 8 * (int64_t)num_sms() / p.n_adapters));
-    adapter_reduce_kernel<<<dim3((unsigned)blocks, (unsigned)p.n_adapters), 256, 0, st>>>(
-        reinterpret_cast<const float4*>(part), plan.seg, p.n_adapters, ranges, n4, reinterpret_cast<float4*>(out));
-    return cudaGetLastError();
+    return launch(adapter_reduce_kernel, dim3((unsigned)blocks, (unsigned)p.n_adapters), 256, 0, st, true,
+                  reinterpret_cast<const float4*>(part), plan.seg, p.n_adapters, ranges, n4,
+                  reinterpret_cast<float4*>(out));
 }
 
 template <typename T>
@@ -1250,7 +1297,7 @@ cudaError_t forward(const moe_adapter_params& p, const T* x, const T* W, const T
                     const int32_t* ids, const float* base, float* y, char* ws, cudaStream_t st) {
     const Layout L = layout_of(p, W != nullptr, false);
     const Plan plan = plan_of(L, ws);
-    const bool few = p.N <= kFewN;
+    const bool few = takes_tokens(p);
     const int slices = few_slices(p.N, p.d_in);
     float* part = reinterpret_cast<float*>(ws + L.u);
     __nv_bfloat16* u = reinterpret_cast<__nv_bfloat16*>(ws + L.u);
@@ -1275,7 +1322,7 @@ cudaError_t forward(const moe_adapter_params& p, const T* x, const T* W, const T
         q.k = 1;
         q.dtype = p.dtype;
         if (sizeof(T) == 2 && !few && tc_tile_rows(q) == 256) {
-            // enough rows for CTA pairs: 4096 x 4096 x 4096 in XX us instead of 114 by single CTAs
+            // enough rows for CTA pairs: 4096 x 4096 x 4096 in 102 us instead of 114 by single CTAs
             const ExpertWeights E{nullptr, nullptr, W, nullptr, nullptr, nullptr};
             e = launch_tc_down(q, DOWN_STORE, p.N, x, nullptr, plan.one_group, plan.one_group + 4, E, nullptr, nullptr,
                                nullptr, y, plan.counters, st, &status);
@@ -1286,19 +1333,9 @@ cudaError_t forward(const moe_adapter_params& p, const T* x, const T* W, const T
         if (e != cudaSuccess) return e;
     }
     if (!few) return launch_expand<T, false>(p, u, B, p.d_out, base, y, W != nullptr, plan, st);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.d_out + 127) / 128), (unsigned)p.N, 1);
-    cfg.blockDim = dim3(128, 1, 1);
-    cfg.stream = st;
-    // set up while the shrink runs (not behind the projection, which does not say when it is done)
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = W ? 0 : 1;
-    e = cudaLaunchKernelEx(&cfg, adapter_few_expand_kernel<T>, (const float*)part, slices, B, ids, (int)p.N, p.d_out,
-                           p.r, p.n_adapters, base, y, (int)(W != nullptr), plan.counters);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch(adapter_few_expand_kernel<T>, dim3((unsigned)((p.d_out + 127) / 128), (unsigned)p.N), 128, 0, st, !W,
+                  (const float*)part, slices, B, ids, (int)p.N, p.d_out, p.r, p.n_adapters, base, y, (int)(W != nullptr),
+                  plan.counters);
 }
 
 template <typename T>
@@ -1318,8 +1355,9 @@ cudaError_t backward(const moe_adapter_params& p, const T* x, const T* W, const 
         __nv_bfloat16* hi = reinterpret_cast<__nv_bfloat16*>(ws + L.hi);
         __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(ws + L.lo);
         const int64_t n = p.N * (int64_t)p.d_out;
-        adapter_split_kernel<<<(unsigned)min64((n / 8 + 255) / 256, (int64_t)num_sms() * 8), 256, 0, st>>>(dy, n, hi, lo);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch(adapter_split_kernel, dim3((unsigned)min64((n / 8 + 255) / 256, (int64_t)num_sms() * 8)), 256, 0, st,
+                   true, dy, n, hi, lo);
+        if (e != cudaSuccess) return e;
         moe_params q{};
         q.N = p.N;
         q.E_r = 1;

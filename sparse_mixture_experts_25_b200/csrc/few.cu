@@ -55,7 +55,7 @@ constexpr int kFewConsumers = 8;                     // consumer warps
 constexpr int kFewProducers = 4;                     // producer warps
 constexpr int kFewThreads = 32 * (kFewConsumers + kFewProducers);
 constexpr int kFewRows = 16;                         // weight rows of a stage
-constexpr int kFewChunk = 2048;                      // most bytes of a row in a stage
+constexpr int kFewChunk = 4096;                      // most bytes of a row in a stage
 constexpr int kFewMaxPaths = kFewMaxTokens * kMaxK;
 
 struct FewArgs {
@@ -73,9 +73,8 @@ struct FewArgs {
     int reject;              // moe_reject_policy (zero or renorm)
     int C;                   // requests an expert takes, at most N
     long long C_stat;        // the capacity as the statistics report it
-    void* h;                 // bf16: three planes of parts; fp32: one plane.  [N k + N][ldh]
-    int64_t h_plane;
-    int ldh;
+    uint8_t* h;              // hidden activations, laid out as the down stages take them (few_h)
+    int h_row;               // bytes set aside for a row
     float* Y;
     unsigned* bar;           // grid barrier, zeroed by the scores kernel
     // records of the routing (workspace)
@@ -205,6 +204,7 @@ struct FewGroup {
     int F;               // hidden units
     int len1, pitch1;    // gate/up pieces (rows of d)
     int len2, pitch2;    // down pieces (rows of F)
+    int hrow;            // bytes of a row of h in a down piece
     int unit_cost;       // relative cost of a gate/up unit
 };
 
@@ -228,12 +228,16 @@ struct FewShared {
 
 // stages of the ring and their size: the rest of the shared memory holds the
 // reductions, which grow with the token tiles NT
-constexpr int few_stages(int) { return 4; }
-constexpr int few_stage_bytes(int NT) { return NT == 1 ? 46 * 1024 : (NT == 2 ? 44 * 1024 : 40 * 1024); }
+// (three large stages beat four of 3/4 the size, 32 tokens of 128 experts 803 ->
+// 751 us, and five or six of 2/3 lose)
+constexpr int kFewStages = 3;
+constexpr int few_stage_bytes(int NT) { return NT == 1 ? 61 * 1024 : (NT == 2 ? 58 * 1024 : 53 * 1024); }
 // gate/up: partial sums of 8 warps, two buffers; down: 8 warps' sums per token (fp32: one)
+constexpr int few_down_rows(bool bf16) { return bf16 ? 2 * kFewRows : kFewRows; }
 constexpr size_t few_red_bytes(bool bf16, int NT) { return (bf16 ? 2 * 8 * 128 * 4 : 8 * kFewRows * 4) * (size_t)NT; }
+static_assert(few_red_bytes(true, 1) >= 8 * 8 * few_down_rows(true) * 4, "the down sums fit where the gate/up ones were");
 constexpr size_t few_smem(bool bf16, int NT) {
-    return few_stages(NT) * (size_t)few_stage_bytes(NT) + few_red_bytes(bf16, NT) + 128 + sizeof(FewShared);
+    return kFewStages * (size_t)few_stage_bytes(NT) + few_red_bytes(bf16, NT) + 128 + sizeof(FewShared);
 }
 
 // a stage position in the ring
@@ -248,27 +252,42 @@ struct RingPos {
     }
 };
 
-// How rows of K elements are cut when a stage holds `rows` of them: `len`
-// elements a piece (equal pieces, multiples of 32 elements), rows `pitch` bytes
-// apart.  The pitch is 64 bytes above a multiple of 128, which puts two
-// consecutive rows on different halves of the banks, so a quarter-warp's
-// 16-byte reads (2 rows x 64 bytes) do not collide.
-__device__ __forceinline__ void few_cut(int K, int es, int rows, int stage_bytes, int& len, int& pitch) {
-    const int cap = min(kFewChunk, (stage_bytes / rows - 64) & ~127) / es;  // elements, a multiple of 32
+// How rows of K elements are cut: `len` elements a piece (equal pieces, multiples
+// of 32 elements, at most what `rows` weight rows and R other rows of `parts`
+// pieces each leave room for), weight rows `pitch` bytes apart.  The pitch is 64 bytes
+// above a multiple of 128, which puts two consecutive rows on different halves of
+// the banks, so a quarter-warp's 16-byte reads (2 rows x 64 bytes) do not collide.
+__device__ __forceinline__ void few_cut(int K, int es, int rows, int R, int parts, int stage_bytes, int& len, int& pitch) {
+    const int room = (stage_bytes - (rows + R) * 64) / (rows + R * parts);
+    const int cap = min(kFewChunk, room & ~127) / es;  // elements, a multiple of 32
     const int n = (K + cap - 1) / cap;
     len = ((K + n - 1) / n + 31) / 32 * 32;
     pitch = cap * es + 64;
+}
+
+// Bytes of a row of h in a down piece: its parts one after another, and 64 more
+// where that is a multiple of 128.  A group's h is stored piece by piece, each
+// with all rows of the group, so that a stage takes its rows of h in one copy.
+__device__ __forceinline__ int few_h_row(int len, int es, int parts) {
+    const int bytes = len * es * parts;
+    return bytes % 128 ? bytes : bytes + 64;
+}
+// more than a row of h can take over all its pieces of at least 64 elements
+inline size_t few_h_bound(int F, int es, int parts) {
+    return ((size_t)F * es * parts + (size_t)(F / 64 + 1) * (32 * es * parts + 64) + 127) / 128 * 128;
 }
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <bool BF16, int NT>
 __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_constant__ FewArgs a) {
-    constexpr int ST = few_stages(NT);
+    constexpr int ST = kFewStages;
     constexpr int SB = few_stage_bytes(NT);
     constexpr int ES = BF16 ? 2 : 4;
     constexpr int PL = BF16 ? 3 : 1;  // parts that h is kept in
-    static_assert(SB / (kFewRows + PL * NT * 8) >= 128 + 64, "a stage holds a piece of every row");
+    constexpr int DR = few_down_rows(BF16);  // weight rows of a down stage
+    static_assert((SB - (DR + NT * 8) * 64) / (DR + PL * NT * 8) >= (BF16 ? 128 : 256),
+                  "a stage holds at least 64 elements of every row");
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;
     float* red = reinterpret_cast<float*>(smem + ST * SB);
@@ -393,8 +412,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         gr.row0 = own ? e_at : n_rows;
         gr.R = own ? e_rows : a.N;
         gr.F = own ? a.d_f : a.d_sh;
-        few_cut(a.d, ES, kFewRows + gr.R, SB, gr.len1, gr.pitch1);
-        few_cut(gr.F, ES, kFewRows + PL * gr.R, SB, gr.len2, gr.pitch2);
+        few_cut(a.d, ES, kFewRows, gr.R, 1, SB, gr.len1, gr.pitch1);
+        few_cut(gr.F, ES, DR, gr.R, PL, SB, gr.len2, gr.pitch2);
+        gr.hrow = few_h_row(gr.len2, ES, PL);
         // a unit's cost: its stages' bytes at an SM's share of the memory (47
         // bytes/ns) or the issue of their copies (15 ns each), whichever is
         // longer, in 1/16 of the first (at most 255)
@@ -470,23 +490,23 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         nj = min(8, (gi == g_to ? j_to : S.grp[gi].F) - j);
         return true;
     };
-    // the output features go in equal tiles of at most 16
+    // the output features go in equal tiles of at most DR
     const int c0 = (int)((int64_t)a.d * blockIdx.x / gridDim.x), c1 = (int)((int64_t)a.d * (blockIdx.x + 1) / gridDim.x);
-    const int c_tiles = (c1 - c0 + kFewRows - 1) / kFewRows;
+    const int c_tiles = (c1 - c0 + DR - 1) / DR;
     const int c_rows = c_tiles ? (c1 - c0 + c_tiles - 1) / c_tiles : 1;
 
     if (warp >= kFewConsumers) {
         // ---- producers: row i of a stage is copied by lane i / 4 of warp i % 4 ----
         const int mine = lane * kFewProducers + warp - kFewConsumers;
-        static_assert(kFewRows + 3 * kFewMaxTokens <= 32 * kFewProducers, "a lane for every row of a stage");
+        static_assert(kFewRows + kFewMaxTokens <= 32 * kFewProducers && DR + 1 <= 32 * kFewProducers, "a lane for every row of a stage");
         RingPos pos;
         int used = 0;  // stages filled at least once
-        // takes the next stage, which this warp copies `rows` pieces of `bytes` to
-        auto open = [&](int rows, uint32_t bytes) {
+        // takes the next stage, which this warp copies its share of `rows` pieces of `bytes`, and `more`, to
+        auto open = [&](int rows, uint32_t bytes, uint32_t more) {
             if (!warp_wait_bounded(&empty[pos.stage], pos.phase ^ 1u, abort_flag, a.counters)) return false;
             if (lane == 0)
                 mbar_expect_tx(&full[pos.stage],
-                               (rows + kFewProducers - 1 - (warp - kFewConsumers)) / kFewProducers * bytes);
+                               (rows + kFewProducers - 1 - (warp - kFewConsumers)) / kFewProducers * bytes + more);
             __syncwarp();
             if (used < ST) ++used;
             return true;
@@ -516,7 +536,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                 }
                 for (int kb = 0; kb < a.d; kb += gr.len1) {
                     const uint32_t bytes = (uint32_t)(min(gr.len1, a.d - kb) * ES);
-                    if (!open(rows, bytes)) return false;
+                    if (!open(rows, bytes, 0)) return false;
                     if (src) copy(pos.stage, slot, gr.pitch1, src + (int64_t)kb * ES, bytes);
                     pos.next(ST);
                 }
@@ -532,30 +552,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                 const int nc = min(c_rows, c1 - c);
                 for (int gi = 0; gi < n_groups; ++gi) {
                     const FewGroup gr = S.grp[gi];
-                    const int total = nc + PL * gr.R;
-                    const uint8_t* src = nullptr;
-                    int slot = 0;
-                    if (mine < nc) {
-                        src = static_cast<const uint8_t*>(gi < n_act ? a.W_d : a.Ws_d) +
-                              ((int64_t)gr.e * a.d + c + mine) * gr.F * ES;
-                        slot = mine;
-                    } else if (mine < total) {
-                        const int r = mine - nc, pl = r >= 2 * gr.R ? 2 : r >= gr.R ? 1 : 0;
-                        src = static_cast<const uint8_t*>(a.h) +
-                              ((int64_t)pl * a.h_plane + (int64_t)(gr.row0 + r - pl * gr.R) * a.ldh) * ES;
-                        slot = kFewRows + r;
-                    }
-                    const bool go = src && (mine < nc ? weights : rows);
-                    for (int kb = 0; kb < gr.F; kb += gr.len2, ++n) {
+                    // weight rows as above; the rows of h, one copy, by the lane after the last of them
+                    const bool mine_w = mine < nc, mine_h = mine == nc;
+                    const uint8_t* src = static_cast<const uint8_t*>(gi < n_act ? a.W_d : a.Ws_d) +
+                                         ((int64_t)gr.e * a.d + c + mine) * gr.F * ES;
+                    const uint32_t h_bytes = (uint32_t)(gr.R * gr.hrow);
+                    const uint8_t* hsrc = a.h + (int64_t)gr.row0 * a.h_row;
+                    const uint32_t mine_more = nc % kFewProducers == warp - kFewConsumers ? h_bytes : 0;
+                    for (int kb = 0; kb < gr.F; kb += gr.len2, ++n, hsrc += h_bytes) {
                         if (n < skip) continue;
                         if (n >= skip + count) return true;
                         const uint32_t bytes = (uint32_t)(min(gr.len2, gr.F - kb) * ES);
                         if (weights) {
-                            if (!open(total, bytes)) return false;
+                            if (!open(nc, bytes, mine_more)) return false;
                             at = pos;
                             pos.next(ST);
+                            if (mine_w) copy(at.stage, mine, gr.pitch2, src + (int64_t)kb * ES, bytes);
                         }
-                        if (go) copy(at.stage, slot, gr.pitch2, src + (int64_t)kb * ES, bytes);
+                        if (rows && mine_h) copy(at.stage, DR, gr.pitch2, hsrc, h_bytes);
                         if (!weights) at.next(ST);
                     }
                 }
@@ -651,35 +665,45 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         RingPos pos;
         const int g = lane >> 2, t = lane & 3;
         const uint4 zero4 = make_uint4(0, 0, 0, 0);
-        // bf16: one group's 16 weight rows against its R token rows (`planes`
-        // parts each), summed over K: the warps take the steps of 32 in turn
-        // (The tensor pipe truncates its running sums, so a piece's products are
-        // summed from zero and added to the sum outside, with rounding: left to
+        // bf16: a stage's WT * 16 weight rows against a group's R token rows
+        // (`planes` parts each), summed over K: the warps take the steps of 32 in
+        // turn.  (The tensor pipe truncates its running sums, so a piece's products
+        // are summed from zero and added to the sum outside, with rounding: left to
         // run over K, Y was off by 2.5e-6 of its norm, ten times as much.)
-        auto mma_rows = [&](auto tiles, int K, int piece, int pitch, int R, auto planes,
-                            float (&sum)[decltype(tiles)::value][4]) {
-            constexpr int M = decltype(tiles)::value;  // column tiles of 8
+        auto mma_rows = [&](auto row_tiles, auto tiles, int K, int piece, int pitch, int R, int row_bytes, auto planes,
+                            float (&sum)[decltype(row_tiles)::value][decltype(tiles)::value][4]) {
+            constexpr int WT = decltype(row_tiles)::value, M = decltype(tiles)::value;  // M column tiles of 8
+            constexpr int P = decltype(planes)::value;
+            constexpr int CH = P > 1 && WT * M <= 2 ? 4 : 2;  // accumulators in turn: more hide more latency
             for (int kb = 0; kb < K; kb += piece) {
                 const int len = min(piece, K - kb);
-                float acc[4][M][4] = {};
+                float acc[CH][WT][M][4] = {};
                 const uint8_t* st = ring + pos.stage * SB;
                 if (warp_wait_bounded(&full[pos.stage], pos.phase, abort_flag, a.counters)) {
-#pragma unroll 4
+#pragma unroll WT * M == 1 ? 4 : 2
                     for (int kk = warp * 32 + t * 8; kk - t * 8 < len; kk += 32 * kFewConsumers) {
                         const bool in = kk < len;  // what lies behind a row's end in the stage is not a number to use
                         const uint8_t* col = st + kk * 2;
-                        auto ld = [&](int row, bool have) {
-                            return have && in ? *reinterpret_cast<const uint4*>(col + row * pitch) : zero4;
+                        auto ld = [&](const uint8_t* p, bool have) {
+                            return have && in ? *reinterpret_cast<const uint4*>(p) : zero4;
                         };
-                        const uint4 lo = ld(g, true), hi = ld(g + 8, true);
+                        uint4 lo[WT], hi[WT];
+#pragma unroll
+                        for (int w = 0; w < WT; ++w) {
+                            lo[w] = ld(col + (w * 16 + g) * pitch, true);
+                            hi[w] = ld(col + (w * 16 + g + 8) * pitch, true);
+                        }
 #pragma unroll
                         for (int n = 0; n < M; ++n) {
                             if (M == 1 || n * 8 < R) {
-                                const int r = n * 8 + g;
-                                mma_step(acc[0][n], acc[1][n], lo, hi, ld(kFewRows + r, r < R));
-                                if (decltype(planes)::value > 1) {
-                                    mma_step(acc[2][n], acc[3][n], lo, hi, ld(kFewRows + 2 * R + r, r < R));
-                                    mma_step(acc[2][n], acc[3][n], lo, hi, ld(kFewRows + R + r, r < R));
+                                const bool have = n * 8 + g < R;
+                                const uint8_t* row = col + WT * 16 * pitch + (n * 8 + g) * row_bytes;
+#pragma unroll
+                                for (int q = P - 1; q >= 0; --q) {  // small parts first
+                                    const uint4 b = ld(row + 2 * q * piece, have);
+#pragma unroll
+                                    for (int w = 0; w < WT; ++w)
+                                        mma_step(acc[q ? CH - 2 : 0][w][n], acc[q ? CH - 1 : 1][w][n], lo[w], hi[w], b);
                                 }
                             }
                         }
@@ -689,29 +713,29 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                 if (lane == 0) mbar_arrive(&empty[pos.stage]);
                 pos.next(ST);
 #pragma unroll
-                for (int n = 0; n < M; ++n)
+                for (int w = 0; w < WT; ++w)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        sum[n][i] += acc[0][n][i] + acc[1][n][i];
-                        if (decltype(planes)::value > 1) sum[n][i] += acc[2][n][i] + acc[3][n][i];
-                    }
+                    for (int n = 0; n < M; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            sum[w][n][i] += acc[0][w][n][i] + acc[1][w][n][i];
+                            if (CH == 4) sum[w][n][i] += acc[CH - 2][w][n][i] + acc[CH - 1][w][n][i];
+                        }
             }
         };
         // fp32: weight rows `warp` and `warp + 8` of the stage against R token rows
-        auto ffma_rows = [&](int K, int piece, int pitch, int R, float (&acc)[2][NT * 8]) {
+        auto ffma_rows = [&](int K, int piece, int pitch, int R, int row_bytes, float (&acc)[2][NT * 8]) {
             for (int kb = 0; kb < K; kb += piece) {
                 const int len = min(piece, K - kb);
                 const uint8_t* st = ring + pos.stage * SB;
                 if (warp_wait_bounded(&full[pos.stage], pos.phase, abort_flag, a.counters)) {
                     for (int kk = lane * 4; kk < len; kk += 128) {
-                        auto ld = [&](int row) {
-                            return *reinterpret_cast<const float4*>(st + row * pitch + kk * 4);
-                        };
-                        const float4 p = ld(warp), q = ld(warp + 8);
+                        auto ld = [&](int at) { return *reinterpret_cast<const float4*>(st + at + kk * 4); };
+                        const float4 p = ld(warp * pitch), q = ld((warp + 8) * pitch);
 #pragma unroll
                         for (int r = 0; r < NT * 8; ++r) {
                             if (r < R) {
-                                const float4 v = ld(kFewRows + r);
+                                const float4 v = ld(kFewRows * pitch + r * row_bytes);
                                 acc[0][r] += p.x * v.x + p.y * v.y + p.z * v.z + p.w * v.w;
                                 acc[1][r] += q.x * v.x + q.y * v.y + q.z * v.z + q.w * v.w;
                             }
@@ -733,24 +757,31 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         };
         const std::integral_constant<int, 1> x_parts{};
         const std::integral_constant<int, PL> h_parts{};
+        const std::integral_constant<int, 1> unit_tiles{};
+        const std::integral_constant<int, DR / 16> down_tiles{};
 
         // gate/up: h of this CTA's hidden units
         int tile = 0, nj;
         for (int gi = S.from[0], j = S.from[1]; unit_tile(gi, j, nj); j += nj, ++tile) {
             const FewGroup gr = S.grp[gi];
-            const int row0 = gr.row0, R = gr.R;
+            const int R = gr.R;
+            // where h of row r and unit j goes: its piece, the row in it, the unit in that
+            auto h_at = [&](int r, int unit) {
+                const int piece = unit / gr.len2;
+                return a.h + (int64_t)gr.row0 * a.h_row + ((int64_t)piece * R + r) * gr.hrow + (unit - piece * gr.len2) * ES;
+            };
             if constexpr (BF16) {
                 // warps' partial sums: [n][16 rows][8 columns], two buffers in turn
                 float* mine = red + ((tile & 1) * 8 + warp) * (NT * 128);
                 by_rows(R, [&](auto tiles) {
                     constexpr int M = decltype(tiles)::value;
-                    float sum[M][4] = {};
-                    mma_rows(tiles, a.d, gr.len1, gr.pitch1, R, x_parts, sum);
+                    float sum[1][M][4] = {};
+                    mma_rows(unit_tiles, tiles, a.d, gr.len1, gr.pitch1, R, gr.pitch1, x_parts, sum);
 #pragma unroll
                     for (int n = 0; n < M; ++n) {
-                        *reinterpret_cast<float2*>(mine + n * 128 + g * 8 + 2 * t) = make_float2(sum[n][0], sum[n][1]);
-                        *reinterpret_cast<float2*>(mine + n * 128 + (g + 8) * 8 + 2 * t) =
-                            make_float2(sum[n][2], sum[n][3]);
+                        const float(&c)[4] = sum[0][n];
+                        *reinterpret_cast<float2*>(mine + n * 128 + g * 8 + 2 * t) = make_float2(c[0], c[1]);
+                        *reinterpret_cast<float2*>(mine + n * 128 + (g + 8) * 8 + 2 * t) = make_float2(c[2], c[3]);
                     }
                 });
                 consumer_sync();
@@ -764,25 +795,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                         zu += p[q * (NT * 128) + 64];
                     }
                     float hv = zg / (1.0f + expf(-zg)) * zu;
-                    __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.h) + (int64_t)(row0 + r) * a.ldh + j + unit;
+                    __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(h_at(r, j + unit));
 #pragma unroll
                     for (int q = 0; q < PL; ++q) {
                         const __nv_bfloat16 part = __float2bfloat16_rn(hv);
-                        h[q * a.h_plane] = part;
+                        h[q * gr.len2] = part;
                         hv -= __bfloat162float(part);
                         hv = isfinite(hv) ? hv : 0.f;  // one that is not finite is its first part
                     }
                 }
             } else {
                 float acc[2][NT * 8] = {};
-                ffma_rows(a.d, gr.len1, gr.pitch1, R, acc);
+                ffma_rows(a.d, gr.len1, gr.pitch1, R, gr.pitch1, acc);
 #pragma unroll
                 for (int r = 0; r < NT * 8; ++r) {
                     if (r < R) {
                         const float zg = warp_sum(acc[0][r]), zu = warp_sum(acc[1][r]);
                         if (lane == (r & 31) && warp < nj)
-                            static_cast<float*>(a.h)[(int64_t)(row0 + r) * a.ldh + j + warp] =
-                                zg / (1.0f + expf(-zg)) * zu;
+                            *reinterpret_cast<float*>(h_at(r, j + warp)) = zg / (1.0f + expf(-zg)) * zu;
                     }
                 }
             }
@@ -816,19 +846,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         // down: this CTA's output features, summed over the experts in order
         for (int c = c0; c < c1; c += c_rows) {
             const int nc = min(c_rows, c1 - c);
-            for (int i = tid; i < (BF16 ? 8 : 1) * NT * 8 * kFewRows; i += 256) yacc[i] = 0.f;
+            for (int i = tid; i < (BF16 ? 8 : 1) * NT * 8 * DR; i += 256) yacc[i] = 0.f;
             consumer_sync();
             for (int gi = 0; gi < n_groups; ++gi) {
                 const bool routed = gi < n_act;
                 const FewGroup gr = S.grp[gi];
                 const int row0 = gr.row0, R = gr.R;
                 if constexpr (BF16) {
-                    // into this warp's sums [token][16 features]: a token has one row in a group
-                    float* mine = yacc + warp * (NT * 8 * kFewRows);
+                    // into this warp's sums [token][DR features]: a token has one row in a group
+                    float* mine = yacc + warp * (NT * 8 * DR);
                     by_rows(R, [&](auto tiles) {
                         constexpr int M = decltype(tiles)::value;
-                        float sum[M][4] = {};
-                        mma_rows(tiles, gr.F, gr.len2, gr.pitch2, R, h_parts, sum);
+                        float sum[DR / 16][M][4] = {};
+                        mma_rows(down_tiles, tiles, gr.F, gr.len2, gr.pitch2, R, gr.hrow, h_parts, sum);
 #pragma unroll
                         for (int n = 0; n < M; ++n)
 #pragma unroll
@@ -837,15 +867,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                                 if (r < R) {
                                     const int tk = routed ? S.row_tok[row0 + r] : r;
                                     const float wt = routed ? S.row_w[row0 + r] : 1.f;
-                                    mine[tk * kFewRows + g] += wt * sum[n][i];
-                                    mine[tk * kFewRows + g + 8] += wt * sum[n][2 + i];
+#pragma unroll
+                                    for (int w = 0; w < DR / 16; ++w) {
+                                        mine[tk * DR + w * 16 + g] += wt * sum[w][n][i];
+                                        mine[tk * DR + w * 16 + g + 8] += wt * sum[w][n][2 + i];
+                                    }
                                 }
                             }
                     });
                     __syncwarp();
                 } else {
                     float acc[2][NT * 8] = {};
-                    ffma_rows(gr.F, gr.len2, gr.pitch2, R, acc);
+                    ffma_rows(gr.F, gr.len2, gr.pitch2, R, gr.hrow, acc);
 #pragma unroll
                     for (int r = 0; r < NT * 8; ++r) {
                         if (r < R) {
@@ -853,20 +886,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                             if (lane == 0) {  // features `warp` and `warp + 8` belong to this warp
                                 const int tk = routed ? S.row_tok[row0 + r] : r;
                                 const float wt = routed ? S.row_w[row0 + r] : 1.f;
-                                yacc[tk * kFewRows + warp] += wt * s0;
-                                yacc[tk * kFewRows + warp + 8] += wt * s1;
+                                yacc[tk * DR + warp] += wt * s0;
+                                yacc[tk * DR + warp + 8] += wt * s1;
                             }
                         }
                     }
                 }
             }
             consumer_sync();
-            for (int i = tid; i < a.N * kFewRows; i += 256) {
-                const int tk = i / kFewRows, f = i % kFewRows;
+            for (int i = tid; i < a.N * DR; i += 256) {
+                const int tk = i / DR, f = i % DR;
                 if (f >= nc) continue;
                 float s = 0.f;
 #pragma unroll
-                for (int q = 0; q < (BF16 ? 8 : 1); ++q) s += yacc[q * (NT * 8 * kFewRows) + i];
+                for (int q = 0; q < (BF16 ? 8 : 1); ++q) s += yacc[q * (NT * 8 * DR) + i];
                 a.Y[(int64_t)tk * a.d + c + f] = s;
             }
             consumer_sync();
@@ -917,7 +950,8 @@ FewLayout few_layout(const moe_params& p, size_t after) {
     L.part = L.bar + 256;
     L.h = L.part + up((size_t)few_score_slices(p.d, p.E_r) * p.N * p.E_r * 4);
     const size_t rows = (size_t)p.N * p.k + (p.d_f_shared > 0 ? (size_t)p.N : 0);
-    L.total = L.h + up(rows * (size_t)std::max(p.d_f, p.d_f_shared) * (p.dtype == MOE_BF16 ? 3 * 2 : 4));
+    L.h_row = few_h_bound(std::max(p.d_f, p.d_f_shared), (int)esize(p.dtype), p.dtype == MOE_BF16 ? 3 : 1);
+    L.total = L.h + up(rows * L.h_row);
     return L;
 }
 
@@ -955,9 +989,8 @@ cudaError_t launch_few(const moe_params& p, int64_t C, const void* x, const void
     a.reject = p.reject_policy;
     a.C = (int)min64(C, p.N);
     a.C_stat = C;
-    a.h = v.base + L.h;
-    a.ldh = std::max(p.d_f, p.d_f_shared);
-    a.h_plane = ((int64_t)p.N * p.k + (p.d_f_shared > 0 ? p.N : 0)) * a.ldh;
+    a.h = reinterpret_cast<uint8_t*>(v.base + L.h);
+    a.h_row = (int)L.h_row;
     a.Y = Y;
     a.bar = reinterpret_cast<unsigned*>(v.base + L.bar);
     a.ids = v.ids;

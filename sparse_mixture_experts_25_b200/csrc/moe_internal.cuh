@@ -229,6 +229,7 @@ struct FewLayout {
     size_t bar;   // grid barrier
     size_t part;  // partial router scores
     size_t h;     // hidden activations
+    size_t h_row; // bytes of one of its rows
     size_t total;
 };
 FewLayout few_layout(const moe_params& p, size_t after);
