@@ -240,6 +240,12 @@ constexpr size_t few_smem(bool bf16, int NT) {
     return kFewStages * (size_t)few_stage_bytes(NT) + few_red_bytes(bf16, NT) + 128 + sizeof(FewShared);
 }
 
+// column tiles of a form for a group's rows (few_layer_kernel's by_rows); 0 stands for one, packed
+template <int M>
+__device__ __forceinline__ constexpr int column_tiles(std::integral_constant<int, M>) {
+    return M ? M : 1;
+}
+
 // a stage position in the ring
 struct RingPos {
     int stage = 0;
@@ -416,10 +422,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         few_cut(gr.F, ES, DR, gr.R, PL, SB, gr.len2, gr.pitch2);
         gr.hrow = few_h_row(gr.len2, ES, PL);
         // a unit's cost: its stages' bytes at an SM's share of the memory (47
-        // bytes/ns) or the issue of their copies (15 ns each), whichever is
+        // bytes/ns) or the issue of their copies (18 ns each), whichever is
         // longer, in 1/16 of the first (at most 255)
         const int n = (a.d + gr.len1 - 1) / gr.len1;
-        const int mem = a.d * (kFewRows * ES) / 47 + 1, issue = n * (kFewRows + gr.R) * 15;
+        const int mem = a.d * (kFewRows * ES) / 47 + 1, issue = n * (kFewRows + gr.R) * 18;
         gr.unit_cost = issue > mem ? min(255, (int)(issue * 16ll / mem)) : 16;
         const int at = own ? e_n + __popc(e_have & ((1u << lane) - 1u)) : n_act;
         S.grp[at] = gr;
@@ -671,9 +677,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         // are summed from zero and added to the sum outside, with rounding: left to
         // run over K, Y was off by 2.5e-6 of its norm, ten times as much.)
         auto mma_rows = [&](auto row_tiles, auto tiles, int K, int piece, int pitch, int R, int row_bytes, auto planes,
-                            float (&sum)[decltype(row_tiles)::value][decltype(tiles)::value][4]) {
-            constexpr int WT = decltype(row_tiles)::value, M = decltype(tiles)::value;  // M column tiles of 8
-            constexpr int P = decltype(planes)::value;
+                            float (&sum)[decltype(row_tiles)::value][column_tiles(decltype(tiles){})][4]) {
+            // M column tiles of 8, or (0) the three parts of one or two rows as the
+            // columns of one tile: part q of row r is column 2 q + r
+            constexpr int WT = decltype(row_tiles)::value, M = column_tiles(tiles);
+            constexpr bool PACKED = decltype(tiles)::value == 0;
+            constexpr int P = PACKED ? 1 : decltype(planes)::value;
             constexpr int CH = P > 1 && WT * M <= 2 ? 4 : 2;  // accumulators in turn: more hide more latency
             for (int kb = 0; kb < K; kb += piece) {
                 const int len = min(piece, K - kb);
@@ -696,8 +705,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
 #pragma unroll
                         for (int n = 0; n < M; ++n) {
                             if (M == 1 || n * 8 < R) {
-                                const bool have = n * 8 + g < R;
-                                const uint8_t* row = col + WT * 16 * pitch + (n * 8 + g) * row_bytes;
+                                const bool have = PACKED ? (g & 1) < R && g < 6 : n * 8 + g < R;
+                                const uint8_t* row = col + WT * 16 * pitch +
+                                                     (PACKED ? (g & 1) * row_bytes + (g >> 1) * 2 * piece
+                                                             : (n * 8 + g) * row_bytes);
 #pragma unroll
                                 for (int q = P - 1; q >= 0; --q) {  // small parts first
                                     const uint4 b = ld(row + 2 * q * piece, have);
@@ -855,10 +866,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                 if constexpr (BF16) {
                     // into this warp's sums [token][DR features]: a token has one row in a group
                     float* mine = yacc + warp * (NT * 8 * DR);
-                    by_rows(R, [&](auto tiles) {
-                        constexpr int M = decltype(tiles)::value;
+                    const auto add = [&](auto tiles) {
+                        constexpr int M = column_tiles(tiles);
                         float sum[DR / 16][M][4] = {};
                         mma_rows(down_tiles, tiles, gr.F, gr.len2, gr.pitch2, R, gr.hrow, h_parts, sum);
+                        if (decltype(tiles)::value == 0) {  // the parts' columns, small ones first, in the lanes of part 0
+#pragma unroll
+                            for (int w = 0; w < DR / 16; ++w)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    float& v = sum[w][0][i];
+                                    const float mid = __shfl_down_sync(0xffffffffu, v, 1);
+                                    v += __shfl_down_sync(0xffffffffu, v, 2) + mid;
+                                }
+                        }
 #pragma unroll
                         for (int n = 0; n < M; ++n)
 #pragma unroll
@@ -874,7 +895,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                                     }
                                 }
                             }
-                    });
+                    };
+                    // one or two rows (a layer of many experts, or one token): all parts in one MMA
+                    if (R <= 2) add(std::integral_constant<int, 0>{});
+                    else by_rows(R, add);
                     __syncwarp();
                 } else {
                     float acc[2][NT * 8] = {};
