@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t* ids, 
         buckets(b, id);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
+            if (b + q * 32 >= t1) break;
             const unsigned same = __match_any_sync(0xffffffffu, id[q]);
             if (id[q] >= 0 && lane == __ffs(same) - 1) cnt[warp * nb + id[q]] += __popc(same);
             __syncwarp();
@@ -218,14 +219,16 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t* ids, 
     }
     if (bad) atomicOr(p.counters + CNT_DEVICE_ERROR, (unsigned long long)DEVERR_BOUNDS);
     __syncthreads();
-    for (int b = tid; b < nb; b += 1024) {  // exclusive over the warps, total in first[b]
-        int s = 0;
-        for (int w = 0; w < 32; ++w) {
-            const int c = cnt[w * nb + b];
-            cnt[w * nb + b] = s;
-            s += c;
+    for (int b = warp; b < nb; b += 32) {  // exclusive over the warps (a lane each), total in first[b]
+        const int c = cnt[lane * nb + b];
+        int v = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
         }
-        first[b] = s;
+        cnt[lane * nb + b] = v - c;
+        if (lane == 31) first[b] = v;
     }
     __syncthreads();
     if (warp == 0) {
@@ -278,6 +281,7 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t* ids, 
         buckets(b, id);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
+            if (b + q * 32 >= t1) break;
             const unsigned same = __match_any_sync(0xffffffffu, id[q]);
             int at = 0;
             if (id[q] >= 0) at = first[id[q]] + cnt[warp * nb + id[q]] + __popc(same & ((1u << lane) - 1u));
@@ -332,12 +336,11 @@ constexpr int kShrinkThreads = 256;
 constexpr int kShrinkFlush = 4;    // stages between additions to the sums
 
 template <typename T, typename TA, bool NN, int NQ>
-__global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(const __grid_constant__ ShrinkArgs a) {
+__device__ __forceinline__ void shrink(const ShrinkArgs& a) {
     constexpr int PA = act_parts<TA, T>(), PB = Parts<T>::self, PF = Parts<T>::f32;
     constexpr int kXPitch = shrink_x_pitch<TA>();
     extern __shared__ __align__(128) uint8_t smem[];
     const cg::cluster_group cluster = cg::this_cluster();
-    in_turn();
     if ((int)blockIdx.x >= *a.p.n_tiles) return;  // the same for the whole cluster
     const Tile tile = a.p.tiles[blockIdx.x];
     if (tile.adapter >= a.n_adapters) return;
@@ -487,6 +490,21 @@ __global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(const __
             *reinterpret_cast<uint32_t*>(a.out + ((int64_t)j * a.N + tile.pos) * r + 2 * i) = out[j];
     }
     cluster.sync();  // the others have read this CTA's sums
+}
+
+template <typename T, int NQ>
+__global__ void __launch_bounds__(kShrinkThreads) adapter_shrink_kernel(const __grid_constant__ ShrinkArgs u) {
+    in_turn();
+    shrink<T, T, false, NQ>(u);
+}
+// u and v in one launch: neither needs the other.  v, the longer one, goes first,
+// and u's CTAs fill in behind it
+template <typename T, int NQ>
+__global__ void __launch_bounds__(kShrinkThreads)
+    adapter_shrink_both_kernel(const __grid_constant__ ShrinkArgs u, const __grid_constant__ ShrinkArgs v) {
+    in_turn();
+    if (blockIdx.z == 0) shrink<T, float, true, NQ>(v);
+    else shrink<T, T, false, NQ>(u);
 }
 
 // ---------------------------------------------------------------------------
@@ -712,6 +730,7 @@ struct GradArgs {
     float* out;               // [n_adapters][r J]
     float* part;              // [ranges + n_adapters][r J]: partial sum of adapter a in range i at i + a
     int J, r, n_adapters;
+    int ranges;
     int64_t N;
     Plan p;
 };
@@ -750,7 +769,7 @@ __device__ __forceinline__ void pair_parts(const Raw4<__nv_bfloat16>& a, const R
 }
 
 template <typename T, typename TZ, bool TRANS, int MT>
-__global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(const __grid_constant__ GradArgs a) {
+__device__ __forceinline__ void grad(const GradArgs& a, int col_block, int range) {
     constexpr int PZ = act_parts<TZ, T>(), PF = Parts<T>::f32;
     constexpr int kInPitch = MT * 32 + 16, kInPart = kGradRows * kInPitch, kStage = grad_stage<PF, MT>();
     constexpr int STEPS = kGradRows / 16;
@@ -758,11 +777,10 @@ __global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(cons
     float* sums = reinterpret_cast<float*>(smem + kGradStages * kStage);  // [MT * 16][128 threads]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int r = a.r, J = a.J;
-    in_turn();
     const int tokens = a.p.seg[a.n_adapters];  // those that have an adapter
-    const int lo = (int)((int64_t)tokens * blockIdx.y / gridDim.y), hi = (int)((int64_t)tokens * (blockIdx.y + 1) / gridDim.y);
+    const int lo = (int)((int64_t)tokens * range / a.ranges), hi = (int)((int64_t)tokens * (range + 1) / a.ranges);
     if (lo >= hi) return;
-    const int col = blockIdx.x * kGradCols + warp * 32 + 4 * g;  // this lane's columns of Z
+    const int col = col_block * kGradCols + warp * 32 + 4 * g;  // this lane's columns of Z
     const TZ* Z = static_cast<const TZ*>(a.Z) + col;
     const bool col_in = col < J;
     // the adapter of position lo: the last one that begins at or before it
@@ -880,9 +898,9 @@ __global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(cons
         __syncthreads();  // the ring is the next adapter's
         // tile n has columns 8 t + n and 8 t + 4 + n of the warp's 32
         const bool alone = seg0 >= lo && seg_end <= hi;
-        float* out = alone ? a.out + (int64_t)adapter * r * J : a.part + ((int64_t)blockIdx.y + adapter) * r * J;
+        float* out = alone ? a.out + (int64_t)adapter * r * J : a.part + ((int64_t)range + adapter) * r * J;
         beg = seg1;
-        const int j = blockIdx.x * kGradCols + warp * 32 + 8 * t;
+        const int j = col_block * kGradCols + warp * 32 + 8 * t;
         if (j < J) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -905,11 +923,28 @@ __global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2) adapter_grad_kernel(cons
     }
 }
 
-// What the ranges left: an adapter's partial sums, range by range, zeros for one
-// without tokens.  CTA (i, a): some of adapter a's elements.
-__global__ void __launch_bounds__(256)
-    adapter_reduce_kernel(const float4* part, const int32_t* seg, int n_adapters, int ranges, int64_t n4, float4* out) {
+// dA and dB in one launch: the first CTAs are dA's
+template <typename T, int MT>
+__global__ void __launch_bounds__(128, MT <= 4 ? 3 : 2)
+    adapter_grad_kernel(const __grid_constant__ GradArgs dA, const __grid_constant__ GradArgs dB) {
     in_turn();
+    const int cols_a = (dA.J + kGradCols - 1) / kGradCols, cols_b = (dB.J + kGradCols - 1) / kGradCols;
+    const int i = blockIdx.x - cols_a * dA.ranges;
+    if (i < 0) grad<T, T, false, MT>(dA, blockIdx.x % cols_a, blockIdx.x / cols_a);
+    else grad<T, float, true, MT>(dB, i % cols_b, i / cols_b);
+}
+
+// What the ranges left: an adapter's partial sums, range by range, zeros for one
+// without tokens.  CTA (i, a, z): some of adapter a's elements of dA or dB.
+__global__ void __launch_bounds__(256)
+    adapter_reduce_kernel(const __grid_constant__ GradArgs dA, const __grid_constant__ GradArgs dB) {
+    in_turn();
+    const GradArgs& a = blockIdx.z ? dB : dA;
+    const float4* part = reinterpret_cast<const float4*>(a.part);
+    float4* out = reinterpret_cast<float4*>(a.out);
+    const int64_t n4 = (int64_t)a.r * a.J / 4;
+    const int32_t* seg = a.p.seg;
+    const int n_adapters = a.n_adapters, ranges = a.ranges;
     const int adapter = blockIdx.y, seg0 = seg[adapter], seg1 = seg[adapter + 1];
     const int64_t tokens = seg[n_adapters];
     float4* to = out + (int64_t)adapter * n4;
@@ -1066,12 +1101,14 @@ int64_t tile_bound(const moe_adapter_params& p) {
     return p.N / kRows + std::min<int64_t>(p.n_adapters + 1, p.N);
 }
 
-// K slices of a shrink: as many CTAs as fit on the GPU at once (two on an SM)
-// for the likely tiles, at least two stages of K each
-int shrink_slices(const moe_adapter_params& p, int K) {
+// K slices of a shrink of `smem` bytes a CTA: as many CTAs as fit on the GPU at
+// once for the likely tiles (up to four on an SM: their registers), at least two
+// stages of K each
+int shrink_slices(const moe_adapter_params& p, int K, size_t smem) {
     const int64_t tiles = p.N / kRows + (std::min<int64_t>(p.n_adapters, p.N) + 1) / 2;
+    const int64_t slots = std::max<int64_t>(1, std::min<int64_t>(p.r <= 16 ? 4 : 2, (227 * 1024) / ((int64_t)smem + 1024))) * num_sms();
     int s = 1;
-    while (s * 2 <= kMaxSlices && s * 2 * tiles <= 2 * num_sms() && K / (s * 2) >= 2 * kShrinkK) s *= 2;
+    while (s * 2 <= kMaxSlices && s * 2 * tiles <= slots && K / (s * 2) >= 2 * kShrinkK) s *= 2;
     return s;
 }
 
@@ -1091,15 +1128,19 @@ int few_slices(int64_t N, int K) {
     return (int)std::max<int64_t>(1, std::min<int64_t>({16, 2 * num_sms() / std::max<int64_t>(N, 1), K / 256}));
 }
 
-// ranges of tokens of a grad: as many as fit on the GPU at once (three CTAs on an
-// SM) with the columns' CTAs, at least 64 tokens each
-int grad_ranges(const moe_adapter_params& p, int J) {
-    const int64_t cols = (J + kGradCols - 1) / kGradCols;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(3 * (int64_t)num_sms() / cols, p.N / 64));
+// ranges of tokens of dA and dB: as many as fit on the GPU at once (three CTAs on
+// an SM) with the columns' CTAs, at least 64 tokens each.  In bf16 a token of dB
+// takes 5/3 of the time of one of dA (both its operands have three parts)
+void grad_ranges(const moe_adapter_params& p, int& a, int& b) {
+    const int64_t slots = 3 * (int64_t)num_sms(), most = std::max<int64_t>(1, p.N / 64);
+    const int64_t ca = (p.d_in + kGradCols - 1) / kGradCols, cb = (p.d_out + kGradCols - 1) / kGradCols;
+    const int wa = 3, wb = p.dtype == MOE_BF16 ? 5 : 3;
+    a = (int)std::max<int64_t>(1, std::min(most, slots * wa / (ca * wa + cb * wb)));
+    b = (int)std::max<int64_t>(1, std::min(most, (slots - ca * a) / cb));
 }
 
 struct Layout {
-    size_t counters, perm, seg, tiles, one_group, u, v, hi, lo, part, total;
+    size_t counters, perm, seg, tiles, one_group, u, v, hi, lo, part_a, part_b, total;
 };
 
 Layout layout_of(const moe_adapter_params& p, bool with_W, bool backward) {
@@ -1125,11 +1166,12 @@ Layout layout_of(const moe_adapter_params& p, bool with_W, bool backward) {
             L.hi = take(N * (size_t)p.d_out * 2);
             L.lo = take(N * (size_t)p.d_out * 2);
         }
-        // partial sums of at most a range's last adapter and the next one's first, so
-        // (ranges + adapters) of them; never written with one range
-        const size_t ra = grad_ranges(p, p.d_in), rb = grad_ranges(p, p.d_out);
-        const size_t pa = ra > 1 ? (ra + p.n_adapters) * p.d_in : 0, pb = rb > 1 ? (rb + p.n_adapters) * p.d_out : 0;
-        L.part = take(std::max(pa, pb) * r * 4);
+        // a partial sum for each range and adapter that meet: at most ranges + adapters
+        // of them; none in one range
+        int ra, rb;
+        grad_ranges(p, ra, rb);
+        L.part_a = take(ra > 1 ? ((size_t)ra + p.n_adapters) * p.d_in * r * 4 : 0);
+        L.part_b = take(rb > 1 ? ((size_t)rb + p.n_adapters) * p.d_out * r * 4 : 0);
     }
     L.total = off;
     return L;
@@ -1170,18 +1212,39 @@ cudaError_t launch_plan(const moe_adapter_params& p, const int32_t* ids, const P
     return launch(adapter_plan_kernel, dim3(1), 1024, smem, st, false, ids, (int)p.N, p.n_adapters, plan);
 }
 
-template <typename T, typename TA, bool NN, int NQ>
-cudaError_t launch_shrink_q(const moe_adapter_params& p, ShrinkArgs a, cudaStream_t st) {
-    constexpr auto kern = adapter_shrink_kernel<T, TA, NN, NQ>;
-    const int slices = shrink_slices(p, a.K);
-    a.slice = ((a.K + slices - 1) / slices + kShrinkK - 1) / kShrinkK * kShrinkK;
-    const size_t smem = std::max((size_t)kStages * shrink_stage<T, TA, NN>(p.r), (size_t)2 * kRows * p.r * 4);
-    constexpr size_t most = std::max((size_t)kStages * shrink_stage<T, TA, NN>(NQ * 8), (size_t)2 * kRows * NQ * 8 * 4);
-    static_assert(most <= 232448, "shared memory per CTA");
-    cudaError_t e = allow_smem_once<kern>(most);
+ShrinkArgs shrink_args(const moe_adapter_params& p, const void* X, const void* M, const float* scale, int K,
+                       __nv_bfloat16* out, const Plan& plan) {
+    ShrinkArgs a{};
+    a.X = X;
+    a.M = M;
+    a.scale = scale;
+    a.K = K;
+    a.r = p.r;
+    a.n_adapters = p.n_adapters;
+    a.N = p.N;
+    a.out = out;
+    a.p = plan;
+    return a;
+}
+
+// u, and v where it is given
+template <typename T, int NQ>
+cudaError_t launch_shrink_q(const moe_adapter_params& p, ShrinkArgs u, ShrinkArgs* v, cudaStream_t st) {
+    constexpr size_t most_u = (size_t)kStages * shrink_stage<T, T, false>(NQ * 8),
+                     most_v = (size_t)kStages * shrink_stage<T, float, true>(NQ * 8),
+                     most_sums = (size_t)2 * kRows * NQ * 8 * 4;
+    static_assert(std::max(most_u, most_v) <= 232448, "shared memory per CTA");
+    size_t smem = std::max((size_t)kStages * shrink_stage<T, T, false>(p.r), (size_t)2 * kRows * p.r * 4);
+    if (v) smem = std::max(smem, (size_t)kStages * shrink_stage<T, float, true>(p.r));
+    cudaError_t e = v ? allow_smem_once<adapter_shrink_both_kernel<T, NQ>>(std::max({most_u, most_v, most_sums}))
+                      : allow_smem_once<adapter_shrink_kernel<T, NQ>>(std::max(most_u, most_sums));
     if (e != cudaSuccess) return e;
+    const int slices = shrink_slices(p, v ? std::min(u.K, v->K) : u.K, smem);
+    auto cut = [&](int K) { return ((K + slices - 1) / slices + kShrinkK - 1) / kShrinkK * kShrinkK; };
+    u.slice = cut(u.K);
+    if (v) v->slice = cut(v->K);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)tile_bound(p), (unsigned)slices, 1);
+    cfg.gridDim = dim3((unsigned)tile_bound(p), (unsigned)slices, v ? 2 : 1);
     cfg.blockDim = dim3(kShrinkThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -1194,27 +1257,17 @@ cudaError_t launch_shrink_q(const moe_adapter_params& p, ShrinkArgs a, cudaStrea
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, kern, a);
+    e = v ? cudaLaunchKernelEx(&cfg, adapter_shrink_both_kernel<T, NQ>, u, *v)
+          : cudaLaunchKernelEx(&cfg, adapter_shrink_kernel<T, NQ>, u);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename T, typename TA, bool NN>
-cudaError_t launch_shrink(const moe_adapter_params& p, const TA* X, const T* M, const float* scale, int K,
-                          __nv_bfloat16* out, const Plan& plan, cudaStream_t st) {
-    ShrinkArgs a{};
-    a.X = X;
-    a.M = M;
-    a.scale = scale;
-    a.K = K;
-    a.r = p.r;
-    a.n_adapters = p.n_adapters;
-    a.N = p.N;
-    a.out = out;
-    a.p = plan;
-    if (p.r <= 16) return launch_shrink_q<T, TA, NN, 2>(p, a, st);
-    if (p.r <= 32) return launch_shrink_q<T, TA, NN, 4>(p, a, st);
-    if (p.r <= 64) return launch_shrink_q<T, TA, NN, 8>(p, a, st);
-    return launch_shrink_q<T, TA, NN, 16>(p, a, st);
+template <typename T>
+cudaError_t launch_shrink(const moe_adapter_params& p, const ShrinkArgs& u, ShrinkArgs* v, cudaStream_t st) {
+    if (p.r <= 16) return launch_shrink_q<T, 2>(p, u, v, st);
+    if (p.r <= 32) return launch_shrink_q<T, 4>(p, u, v, st);
+    if (p.r <= 64) return launch_shrink_q<T, 8>(p, u, v, st);
+    return launch_shrink_q<T, 16>(p, u, v, st);
 }
 
 template <typename T, bool NN, int NK>
@@ -1254,42 +1307,48 @@ cudaError_t launch_expand(const moe_adapter_params& p, const __nv_bfloat16* in, 
     return launch_expand_k<T, NN, 8>(p, a, !add_out, st);
 }
 
-template <typename T, typename TZ, bool TRANS, int MT>
-cudaError_t launch_grad_m(const GradArgs& a, dim3 grid, cudaStream_t st) {
-    constexpr auto kern = adapter_grad_kernel<T, TZ, TRANS, MT>;
+template <typename T, int MT>
+cudaError_t launch_grads_m(const GradArgs& dA, const GradArgs& dB, cudaStream_t st) {
+    constexpr auto kern = adapter_grad_kernel<T, MT>;
     constexpr size_t smem = grad_smem<Parts<T>::f32, MT>();
     static_assert(smem <= 232448, "shared memory per CTA");
     cudaError_t e = allow_smem_once<kern>(smem);
     if (e != cudaSuccess) return e;
-    return launch(kern, grid, 128, smem, st, true, a);
+    const int64_t ctas = (int64_t)((dA.J + kGradCols - 1) / kGradCols) * dA.ranges +
+                         (int64_t)((dB.J + kGradCols - 1) / kGradCols) * dB.ranges;
+    return launch(kern, dim3((unsigned)ctas), 128, smem, st, true, dA, dB);
 }
 
-template <typename T, typename TZ, bool TRANS>
-cudaError_t launch_grad(const moe_adapter_params& p, const __nv_bfloat16* in, const TZ* Z, int J, float* out,
-                        float* part, const Plan& plan, cudaStream_t st) {
-    const int ranges = grad_ranges(p, J);
-    GradArgs a{};
-    a.in = in;
-    a.Z = Z;
-    a.out = out;
-    a.part = part;
-    a.J = J;
-    a.r = p.r;
-    a.n_adapters = p.n_adapters;
-    a.N = p.N;
-    a.p = plan;
-    const dim3 grid((unsigned)((J + kGradCols - 1) / kGradCols), (unsigned)ranges);
-    cudaError_t e = p.r <= 16   ? launch_grad_m<T, TZ, TRANS, 1>(a, grid, st)
-                    : p.r <= 32 ? launch_grad_m<T, TZ, TRANS, 2>(a, grid, st)
-                    : p.r <= 64 ? launch_grad_m<T, TZ, TRANS, 4>(a, grid, st)
-                                : launch_grad_m<T, TZ, TRANS, 8>(a, grid, st);
+template <typename T>
+cudaError_t launch_grads(const moe_adapter_params& p, const __nv_bfloat16* u, const __nv_bfloat16* v, const T* x,
+                         const float* dy, float* dA_out, float* dB_out, float* part_a, float* part_b, const Plan& plan,
+                         cudaStream_t st) {
+    GradArgs dA{};
+    dA.in = v;
+    dA.Z = x;
+    dA.out = dA_out;
+    dA.part = part_a;
+    dA.J = p.d_in;
+    dA.r = p.r;
+    dA.n_adapters = p.n_adapters;
+    dA.N = p.N;
+    dA.p = plan;
+    GradArgs dB = dA;
+    dB.in = u;
+    dB.Z = dy;
+    dB.out = dB_out;
+    dB.part = part_b;
+    dB.J = p.d_out;
+    grad_ranges(p, dA.ranges, dB.ranges);
+    cudaError_t e = p.r <= 16   ? launch_grads_m<T, 1>(dA, dB, st)
+                    : p.r <= 32 ? launch_grads_m<T, 2>(dA, dB, st)
+                    : p.r <= 64 ? launch_grads_m<T, 4>(dA, dB, st)
+                                : launch_grads_m<T, 8>(dA, dB, st);
     if (e != cudaSuccess) return e;
     // a CTA for 1024 of an adapter's elements, fewer where there are many adapters
-    const int64_t n4 = (int64_t)p.r * J / 4;
-    const int64_t blocks = std::min<int64_t>((n4 + 255) / 256, std::max<int64_t>(1, 8 * (int64_t)num_sms() / p.n_adapters));
-    return launch(adapter_reduce_kernel, dim3((unsigned)blocks, (unsigned)p.n_adapters), 256, 0, st, true,
-                  reinterpret_cast<const float4*>(part), plan.seg, p.n_adapters, ranges, n4,
-                  reinterpret_cast<float4*>(out));
+    const int64_t n4 = (int64_t)p.r * std::max(p.d_in, p.d_out) / 4;
+    const int64_t blocks = std::min<int64_t>((n4 + 255) / 256, std::max<int64_t>(1, 4 * (int64_t)num_sms() / p.n_adapters));
+    return launch(adapter_reduce_kernel, dim3((unsigned)blocks, (unsigned)p.n_adapters, 2), 256, 0, st, true, dA, dB);
 }
 
 template <typename T>
@@ -1309,7 +1368,7 @@ cudaError_t forward(const moe_adapter_params& p, const T* x, const T* W, const T
         e = cudaGetLastError();
     } else {
         e = launch_plan(p, ids, plan, st);
-        if (e == cudaSuccess) e = launch_shrink<T, T, false>(p, x, A, scale, p.d_in, u, plan, st);
+        if (e == cudaSuccess) e = launch_shrink<T>(p, shrink_args(p, x, A, scale, p.d_in, u, plan), nullptr, st);
     }
     if (e != cudaSuccess) return e;
     if (W) {
@@ -1346,10 +1405,9 @@ cudaError_t backward(const moe_adapter_params& p, const T* x, const T* W, const 
     const Plan plan = plan_of(L, ws);
     __nv_bfloat16* u = reinterpret_cast<__nv_bfloat16*>(ws + L.u);
     __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(ws + L.v);
-    float* part = reinterpret_cast<float*>(ws + L.part);
     cudaError_t e = launch_plan(p, ids, plan, st);
-    if (e == cudaSuccess) e = launch_shrink<T, T, false>(p, x, A, scale, p.d_in, u, plan, st);
-    if (e == cudaSuccess) e = launch_shrink<T, float, true>(p, dy, B, scale, p.d_out, v, plan, st);
+    ShrinkArgs sv = shrink_args(p, dy, B, scale, p.d_out, v, plan);
+    if (e == cudaSuccess) e = launch_shrink<T>(p, shrink_args(p, x, A, scale, p.d_in, u, plan), &sv, st);
     if (e != cudaSuccess) return e;
     if (W && sizeof(T) == 2) {
         __nv_bfloat16* hi = reinterpret_cast<__nv_bfloat16*>(ws + L.hi);
@@ -1371,8 +1429,8 @@ cudaError_t backward(const moe_adapter_params& p, const T* x, const T* W, const 
                               p.d_in, st);
     }
     if (e == cudaSuccess) e = launch_expand<T, true>(p, v, A, p.d_in, dx_base, dx, W != nullptr, plan, st);
-    if (e == cudaSuccess) e = launch_grad<T, T, false>(p, v, x, p.d_in, dA, part, plan, st);
-    if (e == cudaSuccess) e = launch_grad<T, float, true>(p, u, dy, p.d_out, dB, part, plan, st);
+    if (e == cudaSuccess) e = launch_grads<T>(p, u, v, x, dy, dA, dB, reinterpret_cast<float*>(ws + L.part_a),
+                                            reinterpret_cast<float*>(ws + L.part_b), plan, st);
     return e;
 }
 
