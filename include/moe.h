@@ -655,8 +655,12 @@ MOE_API moe_status moe_backward_check(const moe_params* p, const void* bws, moe_
  *
  * Precision: fp32 accumulation.  16-bit operands are used as they are, fp32 ones
  * (u, v, dy; all of an fp32 call's) to 24 mantissa bits, except that W^T dy of a
- * bf16 call takes dy to 16 bits; the fp32 projection runs on the CUDA cores.  Same inputs give the same bits without W; with W the projection
- * may split K over CTAs (fp32 additions in any order).
+ * bf16 call takes dy to 16 bits; the fp32 projection runs on the CUDA cores.
+ * What is not finite in a token's row makes that token's results, and its
+ * adapter's gradients, not finite (a product of an infinity with an fp32 value
+ * may be NaN), and reaches no other token or adapter.
+ * Same inputs give the same bits without W; with W the projection may split K
+ * over CTAs (fp32 additions in any order).
  * Constraints: d_in, d_out and r multiples of 8, r <= 128, n_adapters <= 1024,
  * d_in and d_out <= 2^23, N < 2^30 (fp32 with W: N <= 65535 * 64); else MOE_ERR_UNSUPPORTED.  Pointers
  * of x, W, A, B, base, y, dy, dx, dA, dB and ws 16-byte aligned.

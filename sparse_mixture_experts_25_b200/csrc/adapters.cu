@@ -108,20 +108,26 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// v = sum of P bf16 parts, each the rounding of what the ones before leave.
+// v = sum of P bf16 parts, each the rounding of what the ones before leave.  The
+// first of three is the value cut off, so that the largest finite ones stay
+// finite (rounded, they would be infinite); the parts are exact all the same.
 // A value that is not finite is its first part; the others are 0.
 template <int P>
 __device__ __forceinline__ void split2(float a, float b, uint32_t (&out)[P]) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        out[i] = pack2(a, b);
+        out[i] = P == 3 && i == 0 ? __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632) : pack2(a, b);
         if (i + 1 < P) {
-            a -= __uint_as_float(out[i] << 16);
-            b -= __uint_as_float(out[i] & 0xffff0000u);
-            const float both = a + b;
-            if (both != both) {  // one was not finite (rare)
-                a = isfinite(a) ? a : 0.f;
-                b = isfinite(b) ? b : 0.f;
+            const float left_a = a - __uint_as_float(out[i] << 16), left_b = b - __uint_as_float(out[i] & 0xffff0000u);
+            const float both = left_a + left_b;
+            if (i == 0 && !isfinite(both)) {  // one was not finite (rare); cut off, a NaN might pass for an infinity
+                if (a != a) out[i] |= 0x7fc0u;
+                if (b != b) out[i] |= 0x7fc00000u;
+                a = isfinite(left_a) ? left_a : 0.f;
+                b = isfinite(left_b) ? left_b : 0.f;
+            } else {
+                a = left_a;
+                b = left_b;
             }
         }
     }

@@ -809,7 +809,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                     __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(h_at(r, j + unit));
 #pragma unroll
                     for (int q = 0; q < PL; ++q) {
-                        const __nv_bfloat16 part = __float2bfloat16_rn(hv);
+                        // the first part is cut off: rounded, the largest finite h would be infinite
+                        const __nv_bfloat16 part = q ? __float2bfloat16_rn(hv) : __float2bfloat16_rz(hv);
                         h[q * gr.len2] = part;
                         hv -= __bfloat162float(part);
                         hv = isfinite(hv) ? hv : 0.f;  // one that is not finite is its first part

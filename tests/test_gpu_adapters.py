@@ -288,3 +288,24 @@ def test_adapters_in_a_graph_and_on_two_streams(N):
         torch.cuda.synchronize()
         assert torch.equal(y, want[i]) and torch.equal(dx, grads[i]["dx"])
         assert torch.equal(dA, grads[i]["dA"]) and torch.equal(dB, grads[i]["dB"])
+
+
+@pytest.mark.parametrize("dtype,N", [("fp32", 20), ("fp32", 300), ("bf16", 300)])
+def test_adapters_take_the_largest_finite_values(dtype, N):
+    t = make(N, 136, 264, 3, 16, dtype, "mixed", False, False)
+    bad = 11
+    t["ids"][bad] = t["ids"][bad + 1] = 1
+    top = torch.finfo(t["x"].dtype).max
+    # values at the end of the range, through weights and beside factors that keep every result inside it
+    t["x"][bad] *= 1e-3
+    t["x"][bad + 1, 3], t["dy"][bad, 5] = top, torch.finfo(torch.float32).max
+    t["A"][:, :, 3] *= 1e-3
+    t["B"][:, 5] *= 1e-3
+    t["dy"][bad + 1] *= 1e-3
+    t["scale"][:] = 1e-3
+    want, tol = reference(t, dtype == "bf16")
+    assert all(bool((v.abs() < 3e38).all()) for v in want.values())
+    d = cuda(t)
+    got = dict(backward(d), y=forward(d))
+    for n, v in want.items():
+        within(n, got[n], v, tol[n])

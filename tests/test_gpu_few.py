@@ -201,3 +201,37 @@ def test_few_in_a_graph_and_on_two_streams():
     fresh = forward(w, dict(a, x=x))[2]
     torch.cuda.synchronize()
     assert torch.equal(Y, fresh) and not torch.equal(Y, Ya)
+
+
+def test_few_takes_hidden_values_at_the_end_of_the_range():
+    # h = (181/128)^2 2^127 is finite, but rounds to an infinity in bf16
+    p = moe.params(1, 8, 8, 1, 1)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(1, 8, **bf)
+    x[0, 0] = 1.0
+    W_g, W_u, W_d = (torch.zeros(1, 8, 8, **bf) for _ in range(3))
+    W_g[0, 3, 0], W_u[0, 3, 0] = 181 / 128 * 2.0 ** 63, 181 / 128 * 2.0 ** 64
+    W_d[0, :, 3] = 2.0 ** -100
+    ws = torch.empty(moe.moe_few_workspace_size(p), dtype=torch.uint8, device="cuda")
+    Y = torch.empty(1, 8, device="cuda")
+    moe.moe_forward_few(p, x, torch.zeros(1, 8, **bf), None, None, W_g, W_u, W_d, None, None, None, Y, ws)
+    assert moe.moe_get_stats(p, ws)[0] == moe.MOE_OK
+    assert bool((Y == (181 / 128) ** 2 * 2.0 ** 27).all())
+
+
+def test_few_many_calls_at_once_end():
+    """Calls on four streams, each of which needs every SM: none waits for another's half."""
+    w = QWEN.scaled("few_at_once", N=32, d=512, d_f=320, E=16, k=4)
+    devs = [{n: parity.to_dev(v) for n, v in si.inputs(w.scaled(w.name, seed=s)).items()} for s in range(4)]
+    want = [forward(w, dev)[2] for dev in devs]
+    bufs = [forward(w, dev) for dev in devs]
+    streams = [torch.cuda.Stream() for _ in devs]
+    torch.cuda.synchronize()
+    for _ in range(25):
+        for s, dev, (p, ws, Y) in zip(streams, devs, bufs):
+            with torch.cuda.stream(s):
+                forward(w, dev, p, ws, Y)
+    torch.cuda.synchronize()
+    for y, (p, ws, Y) in zip(want, bufs):
+        assert moe.moe_get_stats(p, ws)[0] == moe.MOE_OK
+        assert torch.equal(y, Y)
