@@ -1135,10 +1135,12 @@ int few_slices(int64_t N, int K) {
 }
 
 // ranges of tokens of dA and dB: as many as fit on the GPU at once (three CTAs on
-// an SM) with the columns' CTAs, at least 64 tokens each.  In bf16 a token of dB
-// takes 5/3 of the time of one of dA (both its operands have three parts)
+// an SM) with the columns' CTAs, of at least 64 tokens or two adapters each.  In
+// bf16 a token of dB takes 5/3 of the time of one of dA (both its operands have
+// three parts)
 void grad_ranges(const moe_adapter_params& p, int& a, int& b) {
-    const int64_t slots = 3 * (int64_t)num_sms(), most = std::max<int64_t>(1, p.N / 64);
+    const int64_t slots = 3 * (int64_t)num_sms();
+    const int64_t most = std::max<int64_t>({1, p.N / 64, std::min<int64_t>(p.N, p.n_adapters) / 2});
     const int64_t ca = (p.d_in + kGradCols - 1) / kGradCols, cb = (p.d_out + kGradCols - 1) / kGradCols;
     const int wa = 3, wb = p.dtype == MOE_BF16 ? 5 : 3;
     a = (int)std::max<int64_t>(1, std::min(most, slots * wa / (ca * wa + cb * wb)));

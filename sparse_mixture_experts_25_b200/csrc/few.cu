@@ -55,7 +55,6 @@ constexpr int kFewConsumers = 8;                     // consumer warps
 constexpr int kFewProducers = 4;                     // producer warps
 constexpr int kFewThreads = 32 * (kFewConsumers + kFewProducers);
 constexpr int kFewRows = 16;                         // weight rows of a stage
-constexpr int kFewChunk = 4096;                      // most bytes of a row in a stage
 constexpr int kFewMaxPaths = kFewMaxTokens * kMaxK;
 
 struct FewArgs {
@@ -232,12 +231,12 @@ struct FewShared {
 // 751 us, and five or six of 2/3 lose)
 constexpr int kFewStages = 3;
 constexpr int few_stage_bytes(int NT) { return NT == 1 ? 61 * 1024 : (NT == 2 ? 58 * 1024 : 53 * 1024); }
-// gate/up: partial sums of 8 warps, two buffers; down: 8 warps' sums per token (fp32: one)
+// gate/up: partial sums of 8 warps, two buffers; down: 8 warps' sums per token
 constexpr int few_down_rows(bool bf16) { return bf16 ? 2 * kFewRows : kFewRows; }
-constexpr size_t few_red_bytes(bool bf16, int NT) { return (bf16 ? 2 * 8 * 128 * 4 : 8 * kFewRows * 4) * (size_t)NT; }
-static_assert(few_red_bytes(true, 1) >= 8 * 8 * few_down_rows(true) * 4, "the down sums fit where the gate/up ones were");
-constexpr size_t few_smem(bool bf16, int NT) {
-    return kFewStages * (size_t)few_stage_bytes(NT) + few_red_bytes(bf16, NT) + 128 + sizeof(FewShared);
+constexpr size_t few_red_bytes(int NT) { return 2 * 8 * 128 * 4 * (size_t)NT; }
+static_assert(few_red_bytes(1) >= 8 * 8 * few_down_rows(true) * 4, "the down sums fit where the gate/up ones were");
+constexpr size_t few_smem(int NT) {
+    return kFewStages * (size_t)few_stage_bytes(NT) + few_red_bytes(NT) + 128 + sizeof(FewShared);
 }
 
 // column tiles of a form for a group's rows (few_layer_kernel's by_rows); 0 stands for one, packed
@@ -265,7 +264,7 @@ struct RingPos {
 // the banks, so a quarter-warp's 16-byte reads (2 rows x 64 bytes) do not collide.
 __device__ __forceinline__ void few_cut(int K, int es, int rows, int R, int parts, int stage_bytes, int& len, int& pitch) {
     const int room = (stage_bytes - (rows + R) * 64) / (rows + R * parts);
-    const int cap = min(kFewChunk, room & ~127) / es;  // elements, a multiple of 32
+    const int cap = (room & ~127) / es;  // elements, a multiple of 32
     const int n = (K + cap - 1) / cap;
     len = ((K + n - 1) / n + 31) / 32 * 32;
     pitch = cap * es + 64;
@@ -283,6 +282,19 @@ inline size_t few_h_bound(int F, int es, int parts) {
     return ((size_t)F * es * parts + (size_t)(F / 64 + 1) * (32 * es * parts + 64) + 127) / 128 * 128;
 }
 
+// Sums each of N values over the warp's lanes, halving what a lane holds at each
+// step: lane i is left with the sums of values i N / 32 and on, in v[0], v[1] ...
+template <int N, int LEFT = N / 2, int FROM = 16>
+__device__ __forceinline__ void lane_sums(float (&v)[N], int lane) {
+    const bool high = lane & FROM;
+#pragma unroll
+    for (int i = 0; i < LEFT; ++i) {
+        const float theirs = high ? v[i] : v[i + LEFT], mine = high ? v[i + LEFT] : v[i];
+        v[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, FROM);
+    }
+    if constexpr (FROM > 1) lane_sums<N, LEFT / 2, FROM / 2>(v, lane);
+}
+
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <bool BF16, int NT>
@@ -298,13 +310,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     uint8_t* ring = smem;
     float* red = reinterpret_cast<float*>(smem + ST * SB);
     float* yacc = red;  // gate/up is over when the down sums begin
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + ST * SB + few_red_bytes(BF16, NT));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + ST * SB + few_red_bytes(NT));
     uint64_t* empty = full + ST;
     uint64_t* h_ready = empty + ST;
     FewShared& S = *reinterpret_cast<FewShared*>(reinterpret_cast<uint8_t*>(full) + 128);
     static_assert((2 * ST + 1) * 8 <= 128, "barriers");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort_flag = &S.abort_flag;
+    // the output features of a CTA go in equal tiles of at most DR, as many in every
+    // CTA: h is cut into pieces for their size
+    const int c_most = (a.d + gridDim.x - 1) / gridDim.x, c_tiles = (c_most + DR - 1) / DR;
+    const int c_rows = (c_most + c_tiles - 1) / c_tiles;
 
     // ---- routing: every CTA selects all tokens' experts ----
     for (int i = tid; i < kMaxRouterExperts; i += kFewThreads) {
@@ -419,7 +435,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         gr.R = own ? e_rows : a.N;
         gr.F = own ? a.d_f : a.d_sh;
         few_cut(a.d, ES, kFewRows, gr.R, 1, SB, gr.len1, gr.pitch1);
-        few_cut(gr.F, ES, DR, gr.R, PL, SB, gr.len2, gr.pitch2);
+        few_cut(gr.F, ES, c_rows, gr.R, PL, SB, gr.len2, gr.pitch2);
         gr.hrow = few_h_row(gr.len2, ES, PL);
         // a unit's cost: its stages' bytes at an SM's share of the memory (47
         // bytes/ns) or the issue of their copies (18 ns each), whichever is
@@ -496,10 +512,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         nj = min(8, (gi == g_to ? j_to : S.grp[gi].F) - j);
         return true;
     };
-    // the output features go in equal tiles of at most DR
     const int c0 = (int)((int64_t)a.d * blockIdx.x / gridDim.x), c1 = (int)((int64_t)a.d * (blockIdx.x + 1) / gridDim.x);
-    const int c_tiles = (c1 - c0 + DR - 1) / DR;
-    const int c_rows = c_tiles ? (c1 - c0 + c_tiles - 1) / c_tiles : 1;
 
     if (warp >= kFewConsumers) {
         // ---- producers: row i of a stage is copied by lane i / 4 of warp i % 4 ----
@@ -575,7 +588,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                             pos.next(ST);
                             if (mine_w) copy(at.stage, mine, gr.pitch2, src + (int64_t)kb * ES, bytes);
                         }
-                        if (rows && mine_h) copy(at.stage, DR, gr.pitch2, hsrc, h_bytes);
+                        if (rows && mine_h) copy(at.stage, c_rows, gr.pitch2, hsrc, h_bytes);
                         if (!weights) at.next(ST);
                     }
                 }
@@ -671,12 +684,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         RingPos pos;
         const int g = lane >> 2, t = lane & 3;
         const uint4 zero4 = make_uint4(0, 0, 0, 0);
-        // bf16: a stage's WT * 16 weight rows against a group's R token rows
-        // (`planes` parts each), summed over K: the warps take the steps of 32 in
+        // bf16: a stage's `rows` weight rows (WT tiles of 16) against a group's R token
+        // rows (`planes` parts each), summed over K: the warps take the steps of 32 in
         // turn.  (The tensor pipe truncates its running sums, so a piece's products
         // are summed from zero and added to the sum outside, with rounding: left to
         // run over K, Y was off by 2.5e-6 of its norm, ten times as much.)
-        auto mma_rows = [&](auto row_tiles, auto tiles, int K, int piece, int pitch, int R, int row_bytes, auto planes,
+        auto mma_rows = [&](auto row_tiles, auto tiles, int rows, int K, int piece, int pitch, int R, int row_bytes, auto planes,
                             float (&sum)[decltype(row_tiles)::value][column_tiles(decltype(tiles){})][4]) {
             // M column tiles of 8, or (0) the three parts of one or two rows as the
             // columns of one tile: part q of row r is column 2 q + r
@@ -699,14 +712,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                         uint4 lo[WT], hi[WT];
 #pragma unroll
                         for (int w = 0; w < WT; ++w) {
-                            lo[w] = ld(col + (w * 16 + g) * pitch, true);
-                            hi[w] = ld(col + (w * 16 + g + 8) * pitch, true);
+                            lo[w] = ld(col + (w * 16 + g) * pitch, w * 16 + g < rows);
+                            hi[w] = ld(col + (w * 16 + g + 8) * pitch, w * 16 + g + 8 < rows);
                         }
 #pragma unroll
                         for (int n = 0; n < M; ++n) {
                             if (M == 1 || n * 8 < R) {
                                 const bool have = PACKED ? (g & 1) < R && g < 6 : n * 8 + g < R;
-                                const uint8_t* row = col + WT * 16 * pitch +
+                                const uint8_t* row = col + rows * pitch +
                                                      (PACKED ? (g & 1) * row_bytes + (g >> 1) * 2 * piece
                                                              : (n * 8 + g) * row_bytes);
 #pragma unroll
@@ -734,29 +747,69 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                         }
             }
         };
-        // fp32: weight rows `warp` and `warp + 8` of the stage against R token rows
-        auto ffma_rows = [&](int K, int piece, int pitch, int R, int row_bytes, float (&acc)[2][NT * 8]) {
+        // fp32: a stage's `rows` weight rows against R token rows.  A warp has 8 of the
+        // weight rows, T (4 or 8) of the tokens and every KP-th step of 64 of K, so that
+        // a value from shared memory meets T or 8 others.  acc[8 r + i]: token r, weight
+        // row i, summed over this lane's part of K.  A row or token past the last is
+        // taken for the last one, and its sums are not used.  (Two weight rows and all
+        // tokens a warp waited for shared memory: 18 experts of 136 x 6200 and 11 tokens
+        // 564 us instead of 192 to 206, 19 of 4600 x 80 and 18 tokens 128 instead of 52.
+        // At 32 rows the sums still bound it: 2 experts of 7168 x 7168 take 828 us, 4.4
+        // times their bytes.)
+        struct Part {
+            int rg, tg, kp, KP;  // which rows, tokens and steps of K
+        };
+        auto token_groups = [](int R) { return R > 16 ? 4 : R > 8 ? 2 : 1; };
+        auto part_of = [&](int rows, int R) {
+            const int RG = rows > 8 ? 2 : 1, TG = token_groups(R);
+            return Part{warp & (RG - 1), warp / RG & (TG - 1), warp / (RG * TG), kFewConsumers / (RG * TG)};
+        };
+        auto ffma_rows = [&](auto tokens, int rows, int K, int piece, int pitch, int R, int row_bytes,
+                             float (&acc)[decltype(tokens)::value * 8]) __attribute__((always_inline)) {
+            constexpr int T = decltype(tokens)::value;
+            const Part me = part_of(rows, R);
+            const bool mine = me.tg * 8 < R;
+            const int row_last = rows - 1 - me.rg * 8, tok_last = R - 1 - me.tg * 8;
+            int w_at[8], x_at[T];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w_at[i] = (me.rg * 8 + min(i, row_last)) * pitch + lane * 8;
+#pragma unroll
+            for (int r = 0; r < T; ++r) x_at[r] = rows * pitch + (me.tg * 8 + min(r, tok_last)) * row_bytes + lane * 8;
             for (int kb = 0; kb < K; kb += piece) {
                 const int len = min(piece, K - kb);
                 const uint8_t* st = ring + pos.stage * SB;
-                if (warp_wait_bounded(&full[pos.stage], pos.phase, abort_flag, a.counters)) {
-                    for (int kk = lane * 4; kk < len; kk += 128) {
-                        auto ld = [&](int at) { return *reinterpret_cast<const float4*>(st + at + kk * 4); };
-                        const float4 p = ld(warp * pitch), q = ld((warp + 8) * pitch);
+                if (warp_wait_bounded(&full[pos.stage], pos.phase, abort_flag, a.counters) && mine) {
+                    auto step = [&](int kk) __attribute__((always_inline)) {
+                        const uint8_t* at = st + kk * 4;
+                        float2 p[8], v[T];
 #pragma unroll
-                        for (int r = 0; r < NT * 8; ++r) {
-                            if (r < R) {
-                                const float4 v = ld(kFewRows * pitch + r * row_bytes);
-                                acc[0][r] += p.x * v.x + p.y * v.y + p.z * v.z + p.w * v.w;
-                                acc[1][r] += q.x * v.x + q.y * v.y + q.z * v.z + q.w * v.w;
-                            }
-                        }
-                    }
+                        for (int i = 0; i < 8; ++i) p[i] = *reinterpret_cast<const float2*>(at + w_at[i]);
+#pragma unroll
+                        for (int r = 0; r < T; ++r) v[r] = *reinterpret_cast<const float2*>(at + x_at[r]);
+#pragma unroll
+                        for (int r = 0; r < T; ++r)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                acc[r * 8 + i] = fmaf(p[i].x, v[r].x, acc[r * 8 + i]);
+#pragma unroll
+                        for (int r = 0; r < T; ++r)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                acc[r * 8 + i] = fmaf(p[i].y, v[r].y, acc[r * 8 + i]);
+                    };
+                    int kk = me.kp * 64;
+#pragma unroll 1
+                    for (; kk + 64 <= len; kk += me.KP * 64) step(kk);
+                    if (kk + lane * 2 < len) step(kk);  // the last, short one
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[pos.stage]);
                 pos.next(ST);
             }
+        };
+        auto by_tokens = [&](int R, auto f) {
+            if (R <= 4) f(std::integral_constant<int, 4>{});
+            else f(std::integral_constant<int, 8>{});
         };
 
         // the form for a group's rows: as many column tiles as they fill (a
@@ -787,7 +840,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                 by_rows(R, [&](auto tiles) {
                     constexpr int M = decltype(tiles)::value;
                     float sum[1][M][4] = {};
-                    mma_rows(unit_tiles, tiles, a.d, gr.len1, gr.pitch1, R, gr.pitch1, x_parts, sum);
+                    mma_rows(unit_tiles, tiles, kFewRows, a.d, gr.len1, gr.pitch1, R, gr.pitch1, x_parts, sum);
 #pragma unroll
                     for (int n = 0; n < M; ++n) {
                         const float(&c)[4] = sum[0][n];
@@ -817,15 +870,31 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                     }
                 }
             } else {
-                float acc[2][NT * 8] = {};
-                ffma_rows(a.d, gr.len1, gr.pitch1, R, gr.pitch1, acc);
+                // warps' partial sums (those that have a step of K): [tokens][8 rows], two buffers in turn
+                float* mine = red + ((tile & 1) * 8 + warp) * (NT * 128);
+                const Part me = part_of(kFewRows, R);
+                const int len = min(gr.len1, a.d);
+                by_tokens(R, [&](auto tokens) {
+                    constexpr int T = decltype(tokens)::value;
+                    float acc[T * 8] = {};
+                    ffma_rows(tokens, kFewRows, a.d, gr.len1, gr.pitch1, R, gr.pitch1, acc);
+                    if (me.kp * 64 < len) {
+                        lane_sums(acc, lane);
 #pragma unroll
-                for (int r = 0; r < NT * 8; ++r) {
-                    if (r < R) {
-                        const float zg = warp_sum(acc[0][r]), zu = warp_sum(acc[1][r]);
-                        if (lane == (r & 31) && warp < nj)
-                            *reinterpret_cast<float*>(h_at(r, j + warp)) = zg / (1.0f + expf(-zg)) * zu;
+                        for (int i = 0; i < T / 4; ++i) mine[lane * (T / 4) + i] = acc[i];
                     }
+                });
+                consumer_sync();
+                const int unit = tid & 7, r = tid >> 3;
+                if (r < R && unit < nj) {
+                    const int TG = token_groups(R);
+                    const float* p = red + ((tile & 1) * 8 + (r >> 3) * 2) * (NT * 128) + (r & 7) * 8 + unit;
+                    float zg = 0.f, zu = 0.f;
+                    for (int q = 0; q < kFewConsumers && q / (2 * TG) * 64 < len; q += 2 * TG) {
+                        zg += p[q * (NT * 128)];
+                        zu += p[(q + 1) * (NT * 128)];
+                    }
+                    *reinterpret_cast<float*>(h_at(r, j + unit)) = zg / (1.0f + expf(-zg)) * zu;
                 }
             }
         }
@@ -858,19 +927,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         // down: this CTA's output features, summed over the experts in order
         for (int c = c0; c < c1; c += c_rows) {
             const int nc = min(c_rows, c1 - c);
-            for (int i = tid; i < (BF16 ? 8 : 1) * NT * 8 * DR; i += 256) yacc[i] = 0.f;
+            for (int i = tid; i < 8 * NT * 8 * DR; i += 256) yacc[i] = 0.f;
             consumer_sync();
             for (int gi = 0; gi < n_groups; ++gi) {
                 const bool routed = gi < n_act;
                 const FewGroup gr = S.grp[gi];
                 const int row0 = gr.row0, R = gr.R;
+                // into this warp's sums [token][DR features]: a token has one row in a group
+                float* mine = yacc + warp * (NT * 8 * DR);
                 if constexpr (BF16) {
-                    // into this warp's sums [token][DR features]: a token has one row in a group
-                    float* mine = yacc + warp * (NT * 8 * DR);
                     const auto add = [&](auto tiles) {
                         constexpr int M = column_tiles(tiles);
                         float sum[DR / 16][M][4] = {};
-                        mma_rows(down_tiles, tiles, gr.F, gr.len2, gr.pitch2, R, gr.hrow, h_parts, sum);
+                        mma_rows(down_tiles, tiles, c_rows, gr.F, gr.len2, gr.pitch2, R, gr.hrow, h_parts, sum);
                         if (decltype(tiles)::value == 0) {  // the parts' columns, small ones first, in the lanes of part 0
 #pragma unroll
                             for (int w = 0; w < DR / 16; ++w)
@@ -902,20 +971,23 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                     else by_rows(R, add);
                     __syncwarp();
                 } else {
-                    float acc[2][NT * 8] = {};
-                    ffma_rows(gr.F, gr.len2, gr.pitch2, R, gr.hrow, acc);
+                    const Part me = part_of(c_rows, R);
+                    by_tokens(R, [&](auto tokens) {
+                        constexpr int T = decltype(tokens)::value;
+                        float acc[T * 8] = {};
+                        ffma_rows(tokens, c_rows, gr.F, gr.len2, gr.pitch2, R, gr.hrow, acc);
+                        if (me.kp * 64 >= min(gr.len2, gr.F)) return;  // no step of K
+                        lane_sums(acc, lane);
 #pragma unroll
-                    for (int r = 0; r < NT * 8; ++r) {
-                        if (r < R) {
-                            const float s0 = warp_sum(acc[0][r]), s1 = warp_sum(acc[1][r]);
-                            if (lane == 0) {  // features `warp` and `warp + 8` belong to this warp
+                        for (int i = 0; i < T / 4; ++i) {
+                            const int at = lane * (T / 4) + i, r = me.tg * 8 + at / 8, f = me.rg * 8 + at % 8;
+                            if (r < R && f < c_rows) {
                                 const int tk = routed ? S.row_tok[row0 + r] : r;
-                                const float wt = routed ? S.row_w[row0 + r] : 1.f;
-                                yacc[tk * DR + warp] += wt * s0;
-                                yacc[tk * DR + warp + 8] += wt * s1;
+                                mine[tk * DR + f] += (routed ? S.row_w[row0 + r] : 1.f) * acc[i];
                             }
                         }
-                    }
+                    });
+                    __syncwarp();
                 }
             }
             consumer_sync();
@@ -924,7 +996,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                 if (f >= nc) continue;
                 float s = 0.f;
 #pragma unroll
-                for (int q = 0; q < (BF16 ? 8 : 1); ++q) s += yacc[q * (NT * 8 * DR) + i];
+                for (int q = 0; q < 8; ++q) s += yacc[q * (NT * 8 * DR) + i];
                 a.Y[(int64_t)tk * a.d + c + f] = s;
             }
             consumer_sync();
@@ -944,8 +1016,8 @@ int few_score_slices(int d, int E) {
 template <bool BF16, int NT>
 cudaError_t launch_layer(const FewArgs& a, cudaStream_t st) {
     auto kern = few_layer_kernel<BF16, NT>;
-    const size_t smem = few_smem(BF16, NT);
-    static_assert(few_smem(BF16, NT) <= 232448, "shared memory per CTA");
+    const size_t smem = few_smem(NT);
+    static_assert(few_smem(NT) <= 232448, "shared memory per CTA");
     cudaError_t e = allow_smem_once<few_layer_kernel<BF16, NT>>(smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
