@@ -37,7 +37,15 @@
 // The kernels of a call are set up while the one before runs and wait for it
 // themselves (programmatic launches), which saves about half a microsecond each.
 //
-// W runs on the layer's own GEMMs (tcgen05 for bf16, dy as two bf16 parts).
+// W runs on the layer's own GEMMs (tcgen05 for bf16, dy as two bf16 parts): its
+// sums run over all of K in the tensor pipe, which truncates them, so y and dx are
+// 3e-6 to 6e-6 of their norm off there, and 1e-6 or less without W.
+//
+// Measured, replayed from a graph: 16 tokens with 16 adapters (d = 4096, r = 16) 5
+// us; 4096 tokens of 32 adapters through a 4096 x 4096 projection 140 us, 101 of
+// them the projection; gradients of 8192 tokens of four adapters (d = 4096, r = 64)
+// 290 to 340 us, of which the products of parts, 69 GFLOP on mma.sync at about
+// 550 TFLOP/s, are 125 and the bytes 74.
 #include "moe_internal.cuh"
 
 #include <cooperative_groups.h>
@@ -312,6 +320,9 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t* ids, 
 // elements of a row and feeds them to two MMAs, the adapter's elements in the
 // same order of K.  The cluster's CTAs add their sums in slice order through
 // distributed shared memory.
+// Measured: u of 4096 x 4096 bf16, r = 16, 14 to 19 us (33.5 MB); u and v of 8192 x
+// 4096, r = 64, 97 us (201 MB): the MMAs that meet a stage, 2 CTAs of 8 warps on an
+// SM, take longer than its bytes.
 // ---------------------------------------------------------------------------
 struct ShrinkArgs {
     const void* X;
@@ -522,6 +533,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
 // two rows (the four MMA tiles take the columns in that order), so a row is read
 // and written in 64 consecutive bytes; what is added to is fetched two steps
 // ahead.
+// Measured: 4096 x 4096, r = 16, read and written in 26 us (134 MB, 5.2 TB/s).
 // ---------------------------------------------------------------------------
 struct ExpandArgs {
     const __nv_bfloat16* in;  // [parts][N][r]
@@ -729,6 +741,9 @@ __global__ void __launch_bounds__(128, NK == 1 ? 4 : NK <= 4 ? 3 : 2) adapter_ex
 // registers a stage ahead: a lane reads 4 consecutive columns of four rows, and
 // the four MMA tiles take the columns in that order, so a lane's results are 8
 // consecutive columns too.
+// Measured: both gradients of 8192 tokens, r = 64, d = 4096, 162 us with the tensor
+// pipe busy 45% of the time: six of nine products of parts for dB, three for dA, at
+// 12 warps an SM (the sums of a thread take 64 registers and the fetched rows 32).
 // ---------------------------------------------------------------------------
 struct GradArgs {
     const __nv_bfloat16* in;  // [parts][N][r]

@@ -19,8 +19,9 @@
 // sizes: CTA c of G takes its share of the hidden units of all chosen (and
 // shared) experts, each weighted by what its expert's stages cost, then output
 // features [c d / G, (c+1) d / G) of every expert.
-// Producer warps copy pieces of up to 2 KB of 16 weight rows, and of the
-// tokens' rows that they meet, into a ring of stages with bulk copies.  They
+// Producer warps copy pieces of 16 weight rows (down: of up to 32), and of the
+// tokens' rows that they meet, into a ring of stages with bulk copies; a piece is
+// as long as a stage has room for, 1 to 3 KB where there are few tokens.  They
 // run ahead across tiles and experts, and fill the ring with down weights
 // before the grid barrier (only the rows of h wait for it), so the memory stays
 // busy while the other warps reduce and wait.  There are four of them because a
@@ -30,7 +31,8 @@
 //
 // bf16: mma.sync m16n8k16 with the 16 weight rows as M and the tokens as N;
 // the eight consumer warps take K steps of 32 in turn and their partial sums
-// meet in shared memory in warp order.  The tensor pipe is nearly idle here:
+// meet in shared memory in warp order.  The tensor pipe is nearly idle here
+// (7% of its cycles for one token of 8 chosen experts of 4096 x 1536):
 // a tcgen05 tile (M = 64 or 128 rows) would fix the cut at that many rows and
 // leave SMs without work.  A lane reads 8 consecutive K elements of its row
 // (16 bytes) and feeds them to two MMAs; both operands use the same order of K,
@@ -38,7 +40,13 @@
 // rounding it to one bf16 would be the layer's largest error by far, two parts
 // still left Y 2.5e-6 of its norm off, and the third costs one more MMA on a
 // third of the bytes.
-// fp32: FFMA, one warp per two rows, nothing rounded.
+// fp32: FFMA, a warp per eight weight rows and up to eight tokens, nothing rounded.
+//
+// Measured (both launches, replayed from a graph): one token through 8 of 128
+// experts of 4096 x 1536 61 us, 4.9 TB/s (the two kernels, the barrier and the
+// first stages are 10 us of that); 7 tokens of 6 to 8 experts of 4096 x 14336 377
+// us and 32 tokens of 165 of 256 experts of 7168 x 2048 2190 us, both above the
+// 6.55 TB/s of a copy; one fp32 token of a 256 x 512 expert 13.3 us, all latency.
 //
 // No atomics are used on the outputs: results do not depend on the schedule.
 #include "mbarrier.cuh"
