@@ -36,6 +36,11 @@ CASES = {
     "f32_all_rows_shared": SWITCH.scaled("few_f32_all", N=32, d=136, d_f=40, E=3, k=3, c=0.0, d_f_shared=1048),
     "f32_capped": SWITCH.scaled("few_f32_capped", N=20, d=72, d_f=48, E=4, k=2, c=0.5, reject_policy=1,
                                 norm=si.NORM_RENORM),
+    "f32_wide_rows": SWITCH.scaled("few_f32_wide", N=21, d=2056, d_f=72, E=2, k=2, norm=si.NORM_RENORM, c=0.0),
+    "f32_two_tiles": SWITCH.scaled("few_f32_tiles", N=3, d=3208, d_f=328, E=6, k=2, norm=si.NORM_RENORM, c=0.0,
+                                   d_f_shared=72),
+    "f32_long_pieces": SWITCH.scaled("few_f32_long", N=11, d=136, d_f=3400, E=4, k=3, norm=si.NORM_RENORM, c=0.0),
+    "narrow_long_pieces": MIXTRAL.scaled("few_narrow_long", N=6, d=96, d_f=6408, E=5, k=3),
     "one_token_wide": MIXTRAL.scaled("few_one_wide", N=1, d=1032, d_f=2056),
     "one_token_one_expert": MIXTRAL.scaled("few_one_expert", N=1, d=8, d_f=8, E=1, k=1),
     "eight": MIXTRAL.scaled("few_eight", N=8, d=512, d_f=264),
