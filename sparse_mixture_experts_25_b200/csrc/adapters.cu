@@ -817,7 +817,7 @@ __device__ __forceinline__ void grad(const GradArgs& a, int col_block, int range
     for (int beg = lo; beg < hi; ++adapter) {
         const int seg0 = a.p.seg[adapter], seg_end = a.p.seg[adapter + 1];
         if (seg_end <= beg) continue;  // an adapter without tokens
-        const int seg1 = min(seg_end, hi), c0 = 0, c1 = (seg1 - beg + kGradRows - 1) / kGradRows;
+        const int seg1 = min(seg_end, hi), c1 = (seg1 - beg + kGradRows - 1) / kGradRows;
         auto fill = [&](int c) {
             if (c < c1) {
                 const uint32_t st = smem_addr(smem) + c % kGradStages * kStage;
@@ -852,7 +852,7 @@ __device__ __forceinline__ void grad(const GradArgs& a, int col_block, int range
                 }
         };
 #pragma unroll
-        for (int c = 0; c < kGradStages - 1; ++c) fill(c0 + c);
+        for (int c = 0; c < kGradStages - 1; ++c) fill(c);
         float acc[MT][4][4] = {};
         auto flush = [&](bool first, bool last) {
 #pragma unroll
@@ -866,13 +866,11 @@ __device__ __forceinline__ void grad(const GradArgs& a, int col_block, int range
             }
         };
         Raw4<TZ> z[STEPS][4];
-        if (c0 < c1) {
-            copies_wait<kGradStages - 2>();
-            __syncthreads();
-            fetch(c0, z);
-        }
+        copies_wait<kGradStages - 2>();
+        __syncthreads();
+        fetch(0, z);
         bool first = true;
-        for (int c = c0; c < c1; ++c) {
+        for (int c = 0; c < c1; ++c) {
             copies_wait<kGradStages - 3>();  // this stage and the next
             __syncthreads();
             fill(c + kGradStages - 1);
