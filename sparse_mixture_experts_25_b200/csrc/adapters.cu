@@ -729,8 +729,8 @@ __global__ void __launch_bounds__(128, NK == 1 ? 4 : NK <= 4 ? 3 : 2) adapter_ex
 // ---------------------------------------------------------------------------
 // grad: G_a(q, j) = sum over adapter a's tokens of in[pos, q] Z[tok(pos), j]
 //   TRANS = false: dA_a [r, J] from v and x;  TRANS = true: dB_a [J, r] from u and dy
-// A CTA has 128 columns and a range of the sorted tokens, the same for every CTA
-// of the row whatever the adapters' shares (cut by adapter instead, the largest
+// A CTA has 128 columns and a range of the sorted tokens that have an adapter (see
+// ranges_of), the same for every CTA of the row whatever the adapters' shares (cut by adapter instead, the largest
 // one's CTAs ran alone at the end: 143 against 77 us for dB of 8192 tokens of
 // four uneven adapters, r = 64, d = 4096).  An adapter that lies in one range is
 // written to its place; one that continues in others leaves partial sums, at
@@ -789,6 +789,12 @@ __device__ __forceinline__ void pair_parts(const Raw4<__nv_bfloat16>& a, const R
     out[0] = __byte_perm(n < 2 ? a.v.x : a.v.y, n < 2 ? b.v.x : b.v.y, n & 1 ? 0x7632 : 0x5410);
 }
 
+// The ranges that `tokens` adapted tokens go in: as many as the host launched CTAs
+// for, which knows only how many tokens there are in all, but none without a
+// token.  An empty range would write nothing, and the reduction reads all ranges
+// from an adapter's first token to its last
+__device__ __forceinline__ int ranges_of(const GradArgs& a, int tokens) { return min(a.ranges, tokens); }
+
 template <typename T, typename TZ, bool TRANS, int MT>
 __device__ __forceinline__ void grad(const GradArgs& a, int col_block, int range) {
     constexpr int PZ = act_parts<TZ, T>(), PF = Parts<T>::f32;
@@ -799,8 +805,9 @@ __device__ __forceinline__ void grad(const GradArgs& a, int col_block, int range
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int r = a.r, J = a.J;
     const int tokens = a.p.seg[a.n_adapters];  // those that have an adapter
-    const int lo = (int)((int64_t)tokens * range / a.ranges), hi = (int)((int64_t)tokens * (range + 1) / a.ranges);
-    if (lo >= hi) return;
+    const int ranges = ranges_of(a, tokens);
+    if (range >= ranges) return;
+    const int lo = (int)((int64_t)tokens * range / ranges), hi = (int)((int64_t)tokens * (range + 1) / ranges);
     const int col = col_block * kGradCols + warp * 32 + 4 * g;  // this lane's columns of Z
     const TZ* Z = static_cast<const TZ*>(a.Z) + col;
     const bool col_in = col < J;
@@ -963,9 +970,9 @@ __global__ void __launch_bounds__(256)
     float4* out = reinterpret_cast<float4*>(a.out);
     const int64_t n4 = (int64_t)a.r * a.J / 4;
     const int32_t* seg = a.p.seg;
-    const int n_adapters = a.n_adapters, ranges = a.ranges;
     const int adapter = blockIdx.y, seg0 = seg[adapter], seg1 = seg[adapter + 1];
-    const int64_t tokens = seg[n_adapters];
+    const int64_t tokens = seg[a.n_adapters];
+    const int ranges = ranges_of(a, (int)tokens);
     float4* to = out + (int64_t)adapter * n4;
     int first = 0, last = -1;
     if (seg0 < seg1) {
@@ -1149,7 +1156,8 @@ int few_slices(int64_t N, int K) {
 }
 
 // ranges of tokens of dA and dB: as many as fit on the GPU at once (three CTAs on
-// an SM) with the columns' CTAs, of at least 64 tokens or two adapters each.  In
+// an SM) with the columns' CTAs, of at least 64 tokens or two adapters each where
+// every token has an adapter (where fewer have, the kernels' ranges_of).  In
 // bf16 a token of dB takes 5/3 of the time of one of dA (both its operands have
 // three parts)
 void grad_ranges(const moe_adapter_params& p, int& a, int& b) {
