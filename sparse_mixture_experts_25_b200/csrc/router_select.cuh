@@ -54,6 +54,9 @@ __device__ __forceinline__ void select_token(const RouterArgs& a, int64_t t, int
         const int e = lane + 32 * i;
         if (e < E && !isfinite(v[i])) bad = true;
     }
+    // one score that is not finite fails the token: no lane has an expert then
+    // (my_e stays -1), whatever its own scores are
+    bad = __any_sync(0xffffffffu, bad);
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) m = fmaxf(m, v[i]);
@@ -65,7 +68,7 @@ __device__ __forceinline__ void select_token(const RouterArgs& a, int64_t t, int
     // k..k+X-1 are the rerouting candidates (lane r holds rank r)
     const int want = k + (a.X > 1 ? a.X : 1);
     const int rounds = want < E ? want : E;
-    if (!__any_sync(0xffffffffu, bad)) {
+    if (!bad) {
         // order-preserving integer keys (-0 counts as 0), so that the warp's
         // maximum and the lowest index that has it are one instruction each
         auto best = [&](uint32_t& bk, int& be) {
