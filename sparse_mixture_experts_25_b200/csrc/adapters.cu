@@ -119,6 +119,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // v = sum of P bf16 parts, each the rounding of what the ones before leave.  The
 // first of three is the value cut off, so that the largest finite ones stay
 // finite (rounded, they would be infinite); the parts are exact all the same.
+// The first of two is rounded, which keeps 16 bits where cutting off keeps 15,
+// and cut off only where it would be infinite.
 // A value that is not finite is its first part; the others are 0.
 template <int P>
 __device__ __forceinline__ void split2(float a, float b, uint32_t (&out)[P]) {
@@ -126,9 +128,21 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t (&out)[P]) {
     for (int i = 0; i < P; ++i) {
         out[i] = P == 3 && i == 0 ? __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632) : pack2(a, b);
         if (i + 1 < P) {
-            const float left_a = a - __uint_as_float(out[i] << 16), left_b = b - __uint_as_float(out[i] & 0xffff0000u);
+            float left_a = a - __uint_as_float(out[i] << 16), left_b = b - __uint_as_float(out[i] & 0xffff0000u);
             const float both = left_a + left_b;
-            if (i == 0 && !isfinite(both)) {  // one was not finite (rare); cut off, a NaN might pass for an infinity
+            if (i == 0 && !isfinite(both)) {  // one was not finite, or rounded to an infinity (rare)
+                if (P != 3) {
+                    const uint32_t cut_a = __float_as_uint(a) & 0xffff0000u, cut_b = __float_as_uint(b) & 0xffff0000u;
+                    if (isfinite(a) && !isfinite(left_a)) {
+                        out[i] = (out[i] & 0xffff0000u) | cut_a >> 16;
+                        left_a = a - __uint_as_float(cut_a);
+                    }
+                    if (isfinite(b) && !isfinite(left_b)) {
+                        out[i] = (out[i] & 0xffffu) | cut_b;
+                        left_b = b - __uint_as_float(cut_b);
+                    }
+                }
+                // cut off, a NaN might pass for an infinity
                 if (a != a) out[i] |= 0x7fc0u;
                 if (b != b) out[i] |= 0x7fc00000u;
                 a = isfinite(left_a) ? left_a : 0.f;
