@@ -1318,15 +1318,20 @@ template <typename T, bool NN, int NK>
 cudaError_t launch_expand_k(const moe_adapter_params& p, ExpandArgs a, bool behind, cudaStream_t st) {
     constexpr auto kern = adapter_expand_kernel<T, NN, NK>;
     // columns of a CTA: at most what leaves room for five CTAs on an SM, and few
-    // enough that there are CTAs for two waves
+    // enough that there are CTAs for two waves; more where the widest rows would
+    // otherwise go in more spans than a grid has blocks in y
     const int64_t tiles = p.N / kRows + 1;
     auto smem = [](int span) { return (size_t)Parts<T>::self * expand_part<T, NN, NK>(span); };
-    static_assert((size_t)Parts<T>::self * expand_part<T, NN, NK>(128) <= 232448, "shared memory per CTA");
+    auto spans = [&](int span) { return ((int64_t)a.J + span - 1) / span; };
+    static_assert((size_t)Parts<T>::self * expand_part<T, NN, NK>(256) <= 232448, "shared memory per CTA");
+    static_assert(kMaxAdapterWidth / 256 <= 65535, "spans of the widest rows");
     a.span = 512;
-    while (a.span > 128 && (smem(a.span) > 40 * 1024 || tiles * ((a.J + a.span - 1) / a.span) < 2 * num_sms())) a.span /= 2;
-    cudaError_t e = allow_smem_once<kern>(std::max(smem(128), (size_t)100 * 1024));
+    while (a.span > 128 && spans(a.span / 2) <= 65535 &&
+           (smem(a.span) > 40 * 1024 || tiles * spans(a.span) < 2 * num_sms()))
+        a.span /= 2;
+    cudaError_t e = allow_smem_once<kern>(std::max(smem(256), (size_t)100 * 1024));
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)tile_bound(p), (unsigned)((a.J + a.span - 1) / a.span), 1);
+    const dim3 grid((unsigned)tile_bound(p), (unsigned)spans(a.span), 1);
     return launch(kern, grid, 128, smem(a.span), st, behind, a);
 }
 
@@ -1498,8 +1503,8 @@ moe_status check(const moe_adapter_params* p) {
         record_error("moe_adapter: d_in, d_out and r must be multiples of 8");
         return MOE_ERR_UNSUPPORTED;
     }
-    if (p->r > kMaxAdapterRank || p->n_adapters > kMaxAdapters || p->N >= (int64_t)1 << 30 || p->d_in > 1 << 23 ||
-        p->d_out > 1 << 23) {
+    if (p->r > kMaxAdapterRank || p->n_adapters > kMaxAdapters || p->N >= (int64_t)1 << 30 || p->d_in > kMaxAdapterWidth ||
+        p->d_out > kMaxAdapterWidth) {
         record_error("moe_adapter: at most rank 128, 1024 adapters, 2^30 - 1 tokens and widths of 2^23");
         return MOE_ERR_UNSUPPORTED;
     }

@@ -222,6 +222,7 @@ cudaError_t launch_simt_dense(int64_t M, int64_t N, int64_t K, const float* A, i
 // adapters.cu
 constexpr int kMaxAdapters = 1024;
 constexpr int kMaxAdapterRank = 128;
+constexpr int kMaxAdapterWidth = 1 << 23;
 
 // few.cu: the whole layer for at most kFewMaxTokens tokens.  Its part of the
 // workspace follows the layer's own regions.
