@@ -49,7 +49,6 @@
 #include "moe_internal.cuh"
 
 #include <cooperative_groups.h>
-#include <stdio.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -1511,16 +1510,6 @@ moe_status check(const moe_adapter_params* p) {
     return MOE_OK;
 }
 
-bool al16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
-
-moe_status status_of(cudaError_t e, const char* where) {
-    if (e == cudaSuccess) return MOE_OK;
-    char buf[160];
-    snprintf(buf, sizeof(buf), "%s: %s (%d)", where, cudaGetErrorString(e), (int)e);
-    record_error(buf);
-    return MOE_ERR_CUDA;
-}
-
 }  // namespace
 }  // namespace moe
 
@@ -1550,15 +1539,15 @@ moe_status moe_adapter_forward(const moe_adapter_params* p, const void* x, const
     moe_status s = check(p);
     if (s == MOE_OK) s = check_projection(p, W);
     if (s != MOE_OK) return s;
-    if (!ws || !al16(ws)) return MOE_ERR_WORKSPACE;
+    if (!ws || !aligned16(ws)) return MOE_ERR_WORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     (void)cudaGetLastError();
     char* w = static_cast<char*>(ws);
     if (p->N == 0)
-        return status_of(cudaMemsetAsync(w + layout_of(*p, false, false).counters, 0, CNT_COUNT * 8, st),
+        return cuda_status(cudaMemsetAsync(w + layout_of(*p, false, false).counters, 0, CNT_COUNT * 8, st),
                          "moe_adapter_forward memset");
     if (!x || !A || !B || !scale || !ids || !y) return MOE_ERR_INVALID_ARG;
-    if (!al16(x) || !al16(W) || !al16(A) || !al16(B) || !al16(base) || !al16(y)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(W) || !aligned16(A) || !aligned16(B) || !aligned16(base) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
     if (W && base == y) return MOE_ERR_INVALID_ARG;  // the projection is written before base is added
     const cudaError_t e =
         p->dtype == MOE_BF16
@@ -1566,7 +1555,7 @@ moe_status moe_adapter_forward(const moe_adapter_params* p, const void* x, const
                       static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, ids, base, y, w, st)
             : forward(*p, static_cast<const float*>(x), static_cast<const float*>(W), static_cast<const float*>(A),
                       static_cast<const float*>(B), scale, ids, base, y, w, st);
-    return status_of(e, "moe_adapter_forward");
+    return cuda_status(e, "moe_adapter_forward");
 }
 
 moe_status moe_adapter_backward(const moe_adapter_params* p, const void* x, const void* W, const void* A, const void* B,
@@ -1575,8 +1564,8 @@ moe_status moe_adapter_backward(const moe_adapter_params* p, const void* x, cons
     moe_status s = check(p);
     if (s == MOE_OK) s = check_projection(p, W);
     if (s != MOE_OK) return s;
-    if (!ws || !al16(ws)) return MOE_ERR_WORKSPACE;
-    if (!dA || !dB || !al16(dA) || !al16(dB)) return MOE_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+    if (!dA || !dB || !aligned16(dA) || !aligned16(dB)) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     (void)cudaGetLastError();
     char* w = static_cast<char*>(ws);
@@ -1585,10 +1574,10 @@ moe_status moe_adapter_backward(const moe_adapter_params* p, const void* x, cons
         cudaError_t e = cudaMemsetAsync(w + layout_of(*p, false, true).counters, 0, CNT_COUNT * 8, st);
         if (e == cudaSuccess) e = cudaMemsetAsync(dA, 0, n * p->d_in, st);
         if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, n * p->d_out, st);
-        return status_of(e, "moe_adapter_backward memset");
+        return cuda_status(e, "moe_adapter_backward memset");
     }
     if (!x || !A || !B || !scale || !ids || !dy || !dx) return MOE_ERR_INVALID_ARG;
-    if (!al16(x) || !al16(W) || !al16(A) || !al16(B) || !al16(dy) || !al16(dx_base) || !al16(dx))
+    if (!aligned16(x) || !aligned16(W) || !aligned16(A) || !aligned16(B) || !aligned16(dy) || !aligned16(dx_base) || !aligned16(dx))
         return MOE_ERR_INVALID_ARG;
     if (W && dx_base == dx) return MOE_ERR_INVALID_ARG;
     const cudaError_t e =
@@ -1598,7 +1587,7 @@ moe_status moe_adapter_backward(const moe_adapter_params* p, const void* x, cons
                        dx_base, dx, dA, dB, w, st)
             : backward(*p, static_cast<const float*>(x), static_cast<const float*>(W), static_cast<const float*>(A),
                        static_cast<const float*>(B), scale, ids, dy, dx_base, dx, dA, dB, w, st);
-    return status_of(e, "moe_adapter_backward");
+    return cuda_status(e, "moe_adapter_backward");
 }
 
 moe_status moe_adapter_check(const moe_adapter_params* p, const void* ws, moe_stream_t stream) {
@@ -1610,7 +1599,7 @@ moe_status moe_adapter_check(const moe_adapter_params* p, const void* ws, moe_st
     cudaError_t e = cudaMemcpyAsync(cnt, static_cast<const char*>(ws) + layout_of(*p, false, false).counters,
                                     sizeof(cnt), cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) return status_of(e, "moe_adapter_check");
+    if (e != cudaSuccess) return cuda_status(e, "moe_adapter_check");
     if (cnt[CNT_DEVICE_ERROR] & DEVERR_TIMEOUT) return MOE_ERR_TIMEOUT;
     if (cnt[CNT_DEVICE_ERROR] & DEVERR_BOUNDS) return MOE_ERR_INVALID_ARG;
     return MOE_OK;

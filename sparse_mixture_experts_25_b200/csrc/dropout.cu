@@ -17,7 +17,6 @@
 #include "moe_internal.cuh"
 
 #include <math.h>
-#include <stdio.h>
 
 namespace moe {
 namespace {
@@ -160,16 +159,6 @@ DropArgs args_of(const moe_dropout_params& p, const uint64_t* step) {
     return a;
 }
 
-bool al16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
-
-moe_status status_of(cudaError_t e, const char* where) {
-    if (e == cudaSuccess) return MOE_OK;
-    char buf[160];
-    snprintf(buf, sizeof(buf), "%s: %s (%d)", where, cudaGetErrorString(e), (int)e);
-    record_error(buf);
-    return MOE_ERR_CUDA;
-}
-
 }  // namespace
 }  // namespace moe
 
@@ -182,7 +171,7 @@ moe_status moe_dropout_forward(const moe_dropout_params* p, const float* Y, cons
     const moe_status s = check(p);
     if (s != MOE_OK) return s;
     if (p->N == 0) return MOE_OK;
-    if (!Y || !out || !al16(Y) || !al16(residual) || !al16(out) || (reinterpret_cast<uintptr_t>(step) & 7u))
+    if (!Y || !out || !aligned16(Y) || !aligned16(residual) || !aligned16(out) || (reinterpret_cast<uintptr_t>(step) & 7u))
         return MOE_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     (void)cudaGetLastError();
@@ -193,7 +182,7 @@ moe_status moe_dropout_forward(const moe_dropout_params* p, const float* Y, cons
     const cudaError_t e = p->dtype == MOE_BF16
                               ? (residual ? launch<float, __nv_bfloat16, true>(a, st) : launch<float, __nv_bfloat16, false>(a, st))
                               : (residual ? launch<float, float, true>(a, st) : launch<float, float, false>(a, st));
-    return status_of(e, "moe_dropout_forward");
+    return cuda_status(e, "moe_dropout_forward");
 }
 
 moe_status moe_dropout_backward(const moe_dropout_params* p, const void* dout, float* dY, const uint64_t* step,
@@ -201,7 +190,7 @@ moe_status moe_dropout_backward(const moe_dropout_params* p, const void* dout, f
     const moe_status s = check(p);
     if (s != MOE_OK) return s;
     if (p->N == 0) return MOE_OK;
-    if (!dout || !dY || !al16(dout) || !al16(dY) || (reinterpret_cast<uintptr_t>(step) & 7u)) return MOE_ERR_INVALID_ARG;
+    if (!dout || !dY || !aligned16(dout) || !aligned16(dY) || (reinterpret_cast<uintptr_t>(step) & 7u)) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     (void)cudaGetLastError();
     DropArgs a = args_of(*p, step);
@@ -209,7 +198,7 @@ moe_status moe_dropout_backward(const moe_dropout_params* p, const void* dout, f
     a.out = dY;
     const cudaError_t e =
         p->dtype == MOE_BF16 ? launch<__nv_bfloat16, float, false>(a, st) : launch<float, float, false>(a, st);
-    return status_of(e, "moe_dropout_backward");
+    return cuda_status(e, "moe_dropout_backward");
 }
 
 }  // extern "C"

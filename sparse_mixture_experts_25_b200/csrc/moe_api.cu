@@ -148,8 +148,11 @@ namespace {
 thread_local cudaEvent_t g_stage_events[8];
 thread_local char g_last_error[256] = "";
 
+// the caller gets the error as a status; the CUDA runtime must not give it to the
+// program's next call as well
 moe_status fail(cudaError_t e, const char* where) {
     snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%d)", where, cudaGetErrorString(e), (int)e);
+    (void)cudaGetLastError();
     return MOE_ERR_CUDA;
 }
 thread_local int g_stage_event_count = 0;
@@ -172,8 +175,6 @@ inline cudaError_t stage_mark(int i, cudaStream_t st) {
     if (g_stage_event_count >= 5 && i < g_stage_event_count) return cudaEventRecord(g_stage_events[i], st);
     return cudaSuccess;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 moe_status check_params(const moe_params* p) {
     if (!p) return MOE_ERR_INVALID_ARG;
@@ -199,10 +200,6 @@ moe_status check_params(const moe_params* p) {
     if (p->d % 8 || p->d_f % 8 || p->d_f_shared % 8) return MOE_ERR_UNSUPPORTED;
     if ((int64_t)p->N * p->k >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
-}
-
-moe_status cuda_status(cudaError_t e, const char* where) {
-    return e == cudaSuccess ? MOE_OK : fail(e, where);
 }
 
 // exact capacity on the binary value of c (see moe.h)
@@ -238,6 +235,9 @@ int64_t capacity_exact(double c, int64_t N, int k, int E) {
 }  // namespace
 
 namespace moe {
+moe_status cuda_status(cudaError_t e, const char* where) {
+    return e == cudaSuccess ? MOE_OK : fail(e, where);
+}
 void record_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error), "%s", msg); }
 }  // namespace moe
 

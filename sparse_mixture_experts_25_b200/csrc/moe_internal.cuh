@@ -99,6 +99,8 @@ struct WsView {
 
 // Host helpers (moe_api.cu)
 void record_error(const char* msg);  // text returned by moe_last_error on this thread
+moe_status cuda_status(cudaError_t e, const char* where);  // MOE_ERR_CUDA, recorded as `where`, unless e is cudaSuccess
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int dispatch_tile_tokens(int k);
 size_t esize(int dtype);
 bool make_view(const moe_params& p, void* ws, WsView& v);
