@@ -746,8 +746,10 @@ __global__ void __launch_bounds__(128, NK == 1 ? 4 : NK <= 4 ? 3 : 2) adapter_ex
 // ranges_of), the same for every CTA of the row whatever the adapters' shares (cut by adapter instead, the largest
 // one's CTAs ran alone at the end: 143 against 77 us for dB of 8192 tokens of
 // four uneven adapters, r = 64, d = 4096).  An adapter that lies in one range is
-// written to its place; one that continues in others leaves partial sums, at
-// most one per range and adapter met, which the reduction adds in order.  Each
+// written to its place; one that continues in others leaves a partial sum in each,
+// which the reduction adds in order.  Only the first and the last adapter of a
+// range can, so it has a place for one that began before it and a place for one
+// that begins in it and goes on.  Each
 // warp has 32 of the columns and all ranks.  The tokens' parts of u or v, which
 // all warps need, and their places come through a ring of asynchronous copies;
 // a row of Z is used by one warp only and goes from global memory to its
@@ -762,7 +764,8 @@ struct GradArgs {
     const __nv_bfloat16* in;  // [parts][N][r]
     const void* Z;
     float* out;               // [n_adapters][r J]
-    float* part;              // [ranges + n_adapters][r J]: partial sum of adapter a in range i at i + a
+    float* part;              // [ranges][2][r J]: partial sums of the adapter that began before the range
+                              // and of the one that begins in it and goes on
     int J, r, n_adapters;
     int ranges;
     int64_t N;
@@ -937,7 +940,7 @@ __device__ __forceinline__ void grad(const GradArgs& a, int col_block, int range
         __syncthreads();  // the ring is the next adapter's
         // tile n has columns 8 t + n and 8 t + 4 + n of the warp's 32
         const bool alone = seg0 >= lo && seg_end <= hi;
-        float* out = alone ? a.out + (int64_t)adapter * r * J : a.part + ((int64_t)range + adapter) * r * J;
+        float* out = alone ? a.out + (int64_t)adapter * r * J : a.part + ((int64_t)2 * range + (seg0 >= lo)) * r * J;
         beg = seg1;
         const int j = col_block * kGradCols + warp * 32 + 8 * t;
         if (j < J) {
@@ -1002,7 +1005,7 @@ __global__ void __launch_bounds__(256)
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int q = first; q <= last; ++q) {
-            const float4 v = part[((int64_t)q + adapter) * n4 + i];
+            const float4 v = part[((int64_t)2 * q + (q == first)) * n4 + i];
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
@@ -1209,12 +1212,11 @@ Layout layout_of(const moe_adapter_params& p, bool with_W, bool backward) {
             L.hi = take(N * (size_t)p.d_out * 2);
             L.lo = take(N * (size_t)p.d_out * 2);
         }
-        // a partial sum for each range and adapter that meet: at most ranges + adapters
-        // of them; none in one range
+        // two partial sums a range; none in one range
         int ra, rb;
         grad_ranges(p, ra, rb);
-        L.part_a = take(ra > 1 ? ((size_t)ra + p.n_adapters) * p.d_in * r * 4 : 0);
-        L.part_b = take(rb > 1 ? ((size_t)rb + p.n_adapters) * p.d_out * r * 4 : 0);
+        L.part_a = take(ra > 1 ? (size_t)2 * ra * p.d_in * r * 4 : 0);
+        L.part_b = take(rb > 1 ? (size_t)2 * rb * p.d_out * r * 4 : 0);
     }
     L.total = off;
     return L;
