@@ -9,6 +9,7 @@ if libmoe.so cannot be built or loaded, importing this package fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -239,21 +240,36 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device: Optional[int] = None) -> Optional[int]:
+    """device: the current device's index, where the caller has it."""
     if stream is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object on the way
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
-def _enqueue(name: str, params, tensors, stream):
+@functools.lru_cache(maxsize=4096)
+def _workspace_need(size: str, params: bytes, *of) -> int:
+    """Bytes that library function `size` (params, *of) asks for: a function of
+    its arguments, looked up where a call's time is its launches'.  0 where the
+    parameters are refused: the call refuses them too, with its own name."""
+    need = ctypes.c_size_t()
+    status = getattr(lib(), size)(ctypes.cast(params, getattr(lib(), size).argtypes[0]), *of, ctypes.byref(need))
+    return need.value if status == MOE_OK else 0
+
+
+def _enqueue(name: str, params, tensors, stream, size=None, *of):
     """Calls library function `name` (params, the tensors' addresses, stream)
     with the tensors' device current: the library launches on the current
     device and, without a stream, on its current stream.  Host tensors and
-    tensors of several devices are refused.  Returns the status."""
+    tensors of several devices are refused, and a workspace (the last tensor)
+    of fewer bytes than library function `size` (params, *of) asks for.
+    Returns the status."""
     import torch
     index, ptrs = -1, []
     for t in tensors:
@@ -270,11 +286,15 @@ def _enqueue(name: str, params, tensors, stream):
         if not t.is_contiguous():
             raise ValueError("libmoe takes contiguous tensors")
         ptrs.append(t.data_ptr())
+    if size is not None and index >= 0 and t.nbytes < (need := _workspace_need(size, bytes(params), *of)):
+        raise ValueError(f"{name}: expected a workspace of {need} bytes ({size}), got {t.nbytes}")
     fn = getattr(lib(), name)
-    if index >= 0 and index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            return fn(ctypes.byref(params), *ptrs, _stream(stream))
-    return fn(ctypes.byref(params), *ptrs, _stream(stream))
+    if index < 0:
+        return fn(ctypes.byref(params), *ptrs, _stream(stream))
+    if index == torch.cuda.current_device():
+        return fn(ctypes.byref(params), *ptrs, _stream(stream, index))
+    with torch.cuda.device(index):
+        return fn(ctypes.byref(params), *ptrs, _stream(stream, index))
 
 
 def _check(status: int, where: str):
@@ -352,8 +372,8 @@ def moe_few_workspace_size(p: Params) -> int:
 def moe_forward_few(p, x, W_r, b_r, lat, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, Y, ws, stream=None):
     """moe_forward for at most 32 tokens in two launches; ws of
     moe_few_workspace_size bytes (see moe_forward_few in include/moe.h)."""
-    _check(_enqueue("moe_forward_few", p, (x, W_r, b_r, lat, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, Y, ws), stream),
-           "moe_forward_few")
+    _check(_enqueue("moe_forward_few", p, (x, W_r, b_r, lat, W_g, W_u, W_d, Ws_g, Ws_u, Ws_d, Y, ws), stream,
+                    "moe_few_workspace_size"), "moe_forward_few")
 
 
 def moe_forward_begin(p, x, W_r, b_r, lat, counts, ws, stream=None):
@@ -587,7 +607,8 @@ def moe_adapter_forward(ap, x, W, A, B, scale, ids, base, y, ws, stream=None):
     for what, t in (("base", base), ("y", y)):
         if t is not None:
             _typed(what, t, f32, (ap.N, ap.d_out))
-    _check(_enqueue("moe_adapter_forward", ap, (x, W, A, B, scale, ids, base, y, ws), stream), "moe_adapter_forward")
+    _check(_enqueue("moe_adapter_forward", ap, (x, W, A, B, scale, ids, base, y, ws), stream,
+                    "moe_adapter_workspace_size", W is not None), "moe_adapter_forward")
 
 
 def moe_adapter_backward(ap, x, W, A, B, scale, ids, dy, dx_base, dx, dA, dB, ws, stream=None):
@@ -601,8 +622,8 @@ def moe_adapter_backward(ap, x, W, A, B, scale, ids, dy, dx_base, dx, dA, dB, ws
             _typed(what, t, f32, (ap.N, ap.d_in))
     _typed("dA", dA, f32, (ap.n_adapters, ap.r, ap.d_in))
     _typed("dB", dB, f32, (ap.n_adapters, ap.d_out, ap.r))
-    _check(_enqueue("moe_adapter_backward", ap, (x, W, A, B, scale, ids, dy, dx_base, dx, dA, dB, ws), stream),
-           "moe_adapter_backward")
+    _check(_enqueue("moe_adapter_backward", ap, (x, W, A, B, scale, ids, dy, dx_base, dx, dA, dB, ws), stream,
+                    "moe_adapter_backward_workspace_size", W is not None), "moe_adapter_backward")
 
 
 def moe_adapter_check(ap, ws, stream=None) -> int:
