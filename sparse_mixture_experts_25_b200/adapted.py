@@ -6,11 +6,14 @@ Training steps run moe_forward, the adapters beside it and the dropout, and
 AdaptedLayer.backward gives the gradients of the adapters, of x and of the
 layer's own weights.  Serving steps draw nothing and, for at most 32 tokens,
 run the layer in its few-token form.  Everything is enqueued on the current
-stream of the tensors' device; the workspaces are the object's, so one object's
-calls must not be in flight on two streams at once.
+stream of the weights' device, which need not be the current one; tensors of
+another device are refused.  The workspaces are the object's, so one object's
+calls must not be in flight on two streams at once; they are sized for p.N
+tokens, which every call has.
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
@@ -23,6 +26,18 @@ from . import (MOE_ACCEPT_TOKEN, MOE_OK, MOE_REJECT_REROUTE, MoEError, adapter_p
 
 FEW_TOKENS = 32
 WEIGHTS = ("W_r", "b_r", "W_g", "W_u", "W_d", "Ws_g", "Ws_u", "Ws_d")
+
+
+def _on_its_device(method):
+    """Runs a method of an AdaptedLayer with the layer's device current: what it
+    calls is launched on the current device."""
+
+    @functools.wraps(method)
+    def call(self, *args, **kw):
+        with torch.cuda.device(self.device):
+            return method(self, *args, **kw)
+
+    return call
 
 
 class AdaptedLayer:
@@ -39,7 +54,8 @@ class AdaptedLayer:
         n_adapters, r = A.shape[:2]
         self.ap = adapter_params(p.N, p.d, p.d, n_adapters, r, dtype=p.dtype)
         self.rate, self.seed = rate, seed
-        dev = A.device
+        self.device = dev = A.device
+        self._same_device(B=B, scale=scale, **self.w)
         # what the few-token form covers
         self.few = (p.N <= FEW_TOKENS and p.E_r <= 256 and p.reject_policy != MOE_REJECT_REROUTE
                     and p.accept_order == MOE_ACCEPT_TOKEN and p.E_r * p.d_f + p.d_f_shared < 1 << 24)
@@ -51,13 +67,20 @@ class AdaptedLayer:
         self.abws: Optional[torch.Tensor] = None
         self.saved = None
 
+    def _same_device(self, **tensors):
+        for n, t in tensors.items():
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{n}: expected a tensor on {self.device}, got {t.device}")
+
     def _drop(self, rate, offset, row0):
         return dropout_params(self.p.N, self.p.d, rate, seed=self.seed, offset=offset, row0=row0, dtype=self.p.dtype)
 
+    @_on_its_device
     def forward(self, x, ids, residual, lat=None, training: bool = False, offset: int = 0, row0: int = 0):
         """out [N, d] of the layer's dtype.  ids [N] int32 (-1: no adapter).
         training: draws the dropout of call `offset` (row0: the first token's
         row in a sharded batch) and keeps what backward needs."""
+        self._same_device(x=x, ids=ids, residual=residual, lat=lat)
         w = self.w
         call = moe_forward if training or not self.few else moe_forward_few
         call(self.p, x, w["W_r"], w["b_r"], lat, w["W_g"], w["W_u"], w["W_d"], w["Ws_g"], w["Ws_u"], w["Ws_d"],
@@ -69,6 +92,7 @@ class AdaptedLayer:
         self.saved = (x, ids, dp) if training else None
         return out
 
+    @_on_its_device
     def backward(self, dout, aux_coef: float = 0.0):
         """Gradients for dout [N, d] of the layer's dtype, of the last training
         forward: a dict of fp32 tensors (dA, dB, dx and moe_backward's weight
@@ -76,6 +100,7 @@ class AdaptedLayer:
         counts back to the host, so it waits for the forward."""
         if self.saved is None:
             raise ValueError("backward follows a training forward")
+        self._same_device(dout=dout)
         x, ids, dp = self.saved
         p, w, dev = self.p, self.w, x.device
 
@@ -98,6 +123,7 @@ class AdaptedLayer:
                              grads["dA"], grads["dB"], self.abws)
         return grads
 
+    @_on_its_device
     def check(self):
         """Waits for the current stream and raises what the last forward (and
         backward) reported: tokens with non-finite scores, ids out of range, a
