@@ -66,6 +66,7 @@ class AdaptedLayer:
         self.bws: Optional[torch.Tensor] = None
         self.abws: Optional[torch.Tensor] = None
         self.saved = None
+        self.called = False  # until then the workspaces hold nothing
 
     def _same_device(self, **tensors):
         for n, t in tensors.items():
@@ -90,6 +91,7 @@ class AdaptedLayer:
         dp = self._drop(self.rate if training else 0.0, offset, row0)
         moe_dropout_forward(dp, self.Y, residual, out)
         self.saved = (x, ids, dp) if training else None
+        self.called = True
         return out
 
     @_on_its_device
@@ -97,7 +99,9 @@ class AdaptedLayer:
         """Gradients for dout [N, d] of the layer's dtype, of the last training
         forward: a dict of fp32 tensors (dA, dB, dx and moe_backward's weight
         gradients; the residual's gradient is dout).  Reads the forward's row
-        counts back to the host, so it waits for the forward."""
+        counts back to the host, so it waits for the forward.  No other step of
+        this object may run between the two, a replayed one neither: the
+        workspaces are the object's."""
         if self.saved is None:
             raise ValueError("backward follows a training forward")
         self._same_device(dout=dout)
@@ -128,10 +132,14 @@ class AdaptedLayer:
         """Waits for the current stream and raises what the last forward (and
         backward) reported: tokens with non-finite scores, ids out of range, a
         bounded wait that gave up.  Returns the routing statistics."""
+        if not self.called:
+            raise ValueError("check follows a forward")
         status, stats = moe_get_stats(self.p, self.ws)
-        for s, where in ((status, "layer"), (moe_adapter_check(self.ap, self.aws), "adapters")):
+        found = [(status, "layer"), (moe_adapter_check(self.ap, self.aws), "adapters")]
+        if self.bws is not None:
+            found += [(moe_backward_check(self.p, self.bws), "layer gradients"),
+                      (moe_adapter_check(self.ap, self.abws), "adapter gradients")]
+        for s, where in found:
             if s != MOE_OK:
                 raise MoEError(s, where)
-        if self.bws is not None and (s := moe_backward_check(self.p, self.bws)) != MOE_OK:
-            raise MoEError(s, "layer gradients")
         return stats

@@ -76,3 +76,19 @@ def test_tensors_of_another_device_are_refused(made):
     with pytest.raises(ValueError, match="W_u"):
         adapted.AdaptedLayer(m.p, dict(m.w, W_u=m.w["W_u"].to("meta")), m.A, m.B, m.scale)
     assert not made
+
+
+def test_check_reads_what_every_call_reported(made, monkeypatch):
+    m = layer()
+    with pytest.raises(ValueError, match="follows a forward"):  # nothing was written that it could read
+        m.check()
+    m.forward(*batch(), training=True)
+    m.check()
+    assert not any(n == "moe_backward_check" for n, _ in made)
+    m.backward(torch.zeros(N, D))
+    m.check()
+    for bad, where in ((m.aws, "adapters"), (m.abws, "adapter gradients")):
+        monkeypatch.setattr(adapted, "moe_adapter_check",
+                            lambda ap, ws, bad=bad: moe.MOE_ERR_INVALID_ARG if ws is bad else moe.MOE_OK)
+        with pytest.raises(moe.MoEError, match=where):
+            m.check()
