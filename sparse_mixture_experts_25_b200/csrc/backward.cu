@@ -1038,6 +1038,10 @@ moe_status moe_backward(const moe_params* p, float aux_coef, const int32_t* offs
         if (e == cudaSuccess && sh) e = cudaMemsetAsync(gr->dWs_g, 0, sizeof(float) * dfs * d, st);
         if (e == cudaSuccess && sh) e = cudaMemsetAsync(gr->dWs_u, 0, sizeof(float) * dfs * d, st);
         if (e == cudaSuccess && sh) e = cudaMemsetAsync(gr->dWs_d, 0, sizeof(float) * dfs * d, st);
+        // nothing to report (moe_backward_check), whatever the workspace held
+        const size_t at = bwd_layout(*p, kTT).counters;
+        if (e == cudaSuccess && bws_bytes >= at + CNT_COUNT * 8)
+            e = cudaMemsetAsync(static_cast<char*>(bws) + at, 0, CNT_COUNT * 8, st);
         return e == cudaSuccess ? MOE_OK : bwd_fail(e, "memset");
     }
     if (!x || !W_r || !W_g || !W_u || !W_d || !dY) return MOE_ERR_INVALID_ARG;
