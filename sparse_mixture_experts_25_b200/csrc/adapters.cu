@@ -96,14 +96,6 @@ struct Plan {
     unsigned long long* counters;
 };
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void* p) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -1030,31 +1022,6 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const float* v, int6
 // ---------------------------------------------------------------------------
 // A few tokens: u's partial sums per token and K slice, then y
 // ---------------------------------------------------------------------------
-template <typename T>
-__device__ __forceinline__ void load8_f32(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8_f32<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(h[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-template <>
-__device__ __forceinline__ void load8_f32<float>(const float* p, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float4 f = *reinterpret_cast<const float4*>(p + 4 * i);
-        v[4 * i] = f.x;
-        v[4 * i + 1] = f.y;
-        v[4 * i + 2] = f.z;
-        v[4 * i + 3] = f.w;
-    }
-}
-
 // CTA (slice, token): part[slice][token][q] over the slice's K, warp w the ranks w, w + 4, ...
 template <typename T>
 __global__ void __launch_bounds__(128)
@@ -1072,13 +1039,13 @@ __global__ void __launch_bounds__(128)
         float acc[4] = {};
         for (int k = k0 + lane * 8; k < k1; k += 256) {
             float xv[8];
-            load8_f32<T>(x + (int64_t)t * K + k, xv);
+            load8(x + (int64_t)t * K + k, xv);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int q = q0 + 4 * i;
                 if (q < r) {
                     float m[8];
-                    load8_f32<T>(M + (int64_t)q * K + k, m);
+                    load8(M + (int64_t)q * K + k, m);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) acc[i] = fmaf(xv[e], m[e], acc[i]);
                 }
@@ -1121,7 +1088,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll 4
             for (int q = 0; q < r; q += 8) {
                 float m[8];
-                load8_f32<T>(row + q, m);
+                load8(row + q, m);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc = fmaf(u[q + e], m[e], acc);
             }

@@ -40,28 +40,9 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Bounded wait: true when the phase with `parity` completed; false on abort
-// (flag raised elsewhere) or timeout (raises the flag and records it).
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                             unsigned long long* counters,
-                                             unsigned long long limit = kTimeoutNs) {
-    const uint32_t a = smem_u32(bar);
-    if (mbar_try_wait(a, parity)) return true;
-    const unsigned long long t0 = global_timer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(a, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*abort_flag) return false;
-            if (global_timer_ns() - t0 > limit) {
-                *abort_flag = 1;
-                atomicOr(counters + CNT_DEVICE_ERROR, (unsigned long long)DEVERR_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-
-// Warp-collective bounded wait: every lane returns the same result.  The timer
+// Warp-collective bounded wait: true when the phase with `parity` completed;
+// false on abort (flag raised elsewhere) or timeout (raises the flag and records
+// it).  Every lane returns the same result.  The timer
 // is read only once a wait has gone on for a while: reading %globaltimer costs
 // far more than a wait that is already over.
 __device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag,

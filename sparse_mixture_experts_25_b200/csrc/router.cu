@@ -27,24 +27,6 @@ constexpr int kTok = 32;
 constexpr int kThreads = 256;
 constexpr int kKC = 64;
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    float4 a = *reinterpret_cast<const float4*>(p);
-    float4 b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    uint4 u = *reinterpret_cast<const uint4*>(p);
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float2 f = __bfloat1622float2(h[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-
 template <int TT, int TE, typename Tin>
 __global__ void __launch_bounds__(kThreads) router_kernel(RouterArgs a) {
     constexpr int EG = 8 * TT;       // expert groups across the CTA

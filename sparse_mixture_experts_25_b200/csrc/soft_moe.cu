@@ -129,23 +129,6 @@ __global__ void soft_combine_w_kernel(const float* __restrict__ Z, int64_t N, in
 // from the scores), else the identity.
 constexpr int kTT = 64;
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(h[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
 template <typename Tin, bool SOFTMAX>
 __global__ void __launch_bounds__(256) soft_transpose_kernel(const Tin* __restrict__ in, int64_t R, int64_t Cc,
                                                              const float* __restrict__ colmax,
