@@ -592,7 +592,7 @@ MOE_API moe_status moe_soft_check(const moe_soft_params* p, const void* ws, moe_
  * misaligned or smaller than needed),
  * MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA (with moe_last_error).  Asynchronous on
  * `stream`; the library allocates nothing.  N = 0 zeroes the weight
- * gradients and returns.
+ * gradients, clears what moe_backward_check reads and returns.
  */
 typedef struct moe_grads {
     float* dx;      /* [N, d]                       required (may be null when N = 0) */
@@ -656,6 +656,7 @@ MOE_API moe_status moe_backward_check(const moe_params* p, const void* bws, moe_
  * Precision: fp32 accumulation.  16-bit operands are used as they are, fp32 ones
  * (u, v, dy; all of an fp32 call's) to 24 mantissa bits, except that W^T dy of a
  * bf16 call takes dy to 16 bits; the fp32 projection runs on the CUDA cores.
+ * Operands up to the largest finite value are taken as such.
  * What is not finite in a token's row makes that token's results, and its
  * adapter's gradients, not finite (a product of an infinity with an fp32 value
  * may be NaN), and reaches no other token or adapter.
@@ -680,7 +681,8 @@ typedef struct moe_adapter_params {
     int32_t reserved;    /* 0                                                  */
 } moe_adapter_params;
 
-/* Workspace bytes (host); with_W: whether the calls give a projection. */
+/* Workspace bytes (host); with_W: whether the calls give a projection.  The calls
+ * are not told the size of ws: it is the caller's to make it as large as this. */
 MOE_API moe_status moe_adapter_workspace_size(const moe_adapter_params* p, int with_W, size_t* bytes);
 MOE_API moe_status moe_adapter_backward_workspace_size(const moe_adapter_params* p, int with_W, size_t* bytes);
 

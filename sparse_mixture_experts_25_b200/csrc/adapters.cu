@@ -27,8 +27,9 @@
 // would be mostly padding at these ranks: the tensor pipe is not what bounds.)
 // u and v are stored as such parts, in the sorted order.  The tensor pipe
 // truncates its running sums: left to run over K = 1000 in fp32, y was off by
-// 4.9e-6 of its norm.  So a long sum is kept outside: the products of one stage
-// are summed from zero (small parts first) and added to it with rounding.
+// 4.9e-6 of its norm.  So a long sum is kept outside: the products of up to four
+// stages (256 K of a shrink, 128 tokens of a gradient; a stage's small parts
+// first) are summed from zero and added to it with rounding.
 //
 // Few tokens take another form (see takes_tokens): no sort, one CTA per token
 // and slice of K, then one thread per output; two launches instead of three, and
@@ -38,14 +39,17 @@
 // themselves (programmatic launches), which saves about half a microsecond each.
 //
 // W runs on the layer's own GEMMs (tcgen05 for bf16, dy as two bf16 parts): its
-// sums run over all of K in the tensor pipe, which truncates them, so y and dx are
-// 3e-6 to 6e-6 of their norm off there, and 1e-6 or less without W.
+// sums run over all of K in the tensor pipe, which truncates them, so y is 4.4e-6 of
+// its norm off at K = 4096 and dx 5.0e-6 (1.5e-6 and 2.9e-6 at 1536; 1e-6 or less
+// without W).  Two parts of dy are a choice: their 16 bits are 2.4e-6 of that, added
+// at right angles, and a third would take half of that GEMM's time again (26 us of
+// 118, 2047 tokens, 4096 to 1536).
 //
 // Measured, replayed from a graph: 16 tokens with 16 adapters (d = 4096, r = 16) 5
-// us; 4096 tokens of 32 adapters through a 4096 x 4096 projection 140 us, 101 of
-// them the projection; gradients of 8192 tokens of four adapters (d = 4096, r = 64)
-// 290 to 340 us, of which the products of parts, 69 GFLOP on mma.sync at about
-// 550 TFLOP/s, are 125 and the bytes 74.
+// us; 4096 tokens of 32 adapters through a 4096 x 4096 projection 141 to 155 us, 101
+// of them the projection; gradients of 8192 tokens of four adapters (d = 4096, r =
+// 64) 280 to 350 us by how many of the tokens have an adapter, of which the products
+// of parts, 69 GFLOP on mma.sync at about 550 TFLOP/s, are 125 and the bytes 74.
 #include "moe_internal.cuh"
 
 #include <cooperative_groups.h>

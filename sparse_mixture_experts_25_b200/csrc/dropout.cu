@@ -12,7 +12,7 @@
 // s-byte type, read and written once.  A thread has 8 consecutive elements:
 // 16-byte accesses, and two generator calls of 20 32-bit products.  A dropped
 // element is selected away, not multiplied, so an infinity there leaves 0.
-// Measured: 8192 x 4096 bf16 with a residual 40 us (268 MB, 6.6 TB/s), the gradient
+// Measured: 8192 x 4096 bf16 with a residual 40 us (268 MB, 6.7 TB/s), the gradient
 // of 8191 x 7168 60 us (352 MB, 5.9 TB/s; the generator keeps the SMs two thirds busy).
 #include "moe_internal.cuh"
 
