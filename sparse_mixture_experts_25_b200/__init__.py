@@ -286,8 +286,11 @@ def _enqueue(name: str, params, tensors, stream, size=None, *of):
         if not t.is_contiguous():
             raise ValueError("libmoe takes contiguous tensors")
         ptrs.append(t.data_ptr())
-    if size is not None and index >= 0 and t.nbytes < (need := _workspace_need(size, bytes(params), *of)):
-        raise ValueError(f"{name}: expected a workspace of {need} bytes ({size}), got {t.nbytes}")
+    ws = tensors[-1]
+    if size is not None and not (ws is None or isinstance(ws, int)):
+        need = _workspace_need(size, bytes(params), *of)
+        if ws.nbytes < need:
+            raise ValueError(f"{name}: expected a workspace of {need} bytes ({size}), got {ws.nbytes}")
     fn = getattr(lib(), name)
     if index < 0:
         return fn(ctypes.byref(params), *ptrs, _stream(stream))

@@ -61,3 +61,20 @@ def test_few_workspaces_are_measured():
     # counted in bytes whatever the tensor's type is
     with pytest.raises(ValueError, match="workspace of"):
         moe.moe_forward_few(p, *args, Described(torch.int32, moe.moe_few_workspace_size(p) // 4 - 1))
+
+
+@pytest.mark.parametrize("ws", [None, 256 + 8], ids=["missing", "misaligned address"])
+def test_a_workspace_without_a_size_is_the_librarys_to_refuse(ws, monkeypatch):
+    """None and plain addresses, which the binding takes too: the library's status."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    ap, p = moe.adapter_params(5, 64, 72, 4, 8), moe.params(N=8, d=64, d_f=96, E_r=4, k=2)
+    forward, backward = adapter_tensors(ap, False)
+    bf = torch.bfloat16
+    few = (Described(bf, 8, 64), Described(bf, 4, 64), None, None, Described(bf, 4, 96, 64), Described(bf, 4, 96, 64),
+           Described(bf, 4, 64, 96), None, None, None, Described(torch.float32, 8, 64))
+    for call in (lambda: moe.moe_adapter_forward(ap, **forward, ws=ws, stream=0),
+                 lambda: moe.moe_adapter_backward(ap, **backward, ws=ws, stream=0),
+                 lambda: moe.moe_forward_few(p, *few, ws, stream=0)):
+        with pytest.raises(moe.MoEError) as e:
+            call()
+        assert e.value.status == moe.MOE_ERR_WORKSPACE
