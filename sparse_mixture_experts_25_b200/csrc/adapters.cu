@@ -1029,8 +1029,8 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const float* v, int6
 // CTA (slice, token): part[slice][token][q] over the slice's K, warp w the ranks w, w + 4, ...
 template <typename T>
 __global__ void __launch_bounds__(128)
-    adapter_few_shrink_kernel(const T* x, const T* A, const float* scale, const int32_t* ids, int N, int K, int r,
-                              int n_adapters, int slice, float* part, unsigned long long* counters) {
+    adapter_few_shrink_kernel(const T* x, const T* A, const int32_t* ids, int N, int K, int r, int n_adapters, int slice,
+                              float* part, unsigned long long* counters) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t = blockIdx.y;
     if (blockIdx.x == 0 && t == 0 && tid < CNT_COUNT) counters[tid] = 0ull;
@@ -1060,21 +1060,22 @@ __global__ void __launch_bounds__(128)
             float s = acc[i];
 #pragma unroll
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0 && q0 + 4 * i < r) out[q0 + 4 * i] = s * scale[id];
+            if (lane == 0 && q0 + 4 * i < r) out[q0 + 4 * i] = s;
         }
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(128)
-    adapter_few_expand_kernel(const float* part, int slices, const T* B, const int32_t* ids, int N, int J, int r,
-                              int n_adapters, const float* base, float* out, int add_out,
+    adapter_few_expand_kernel(const float* part, int slices, const T* B, const float* scale, const int32_t* ids, int N,
+                              int J, int r, int n_adapters, const float* base, float* out, int add_out,
                               unsigned long long* counters) {
     __shared__ float u[kMaxAdapterRank];
     const int tid = threadIdx.x, t = blockIdx.y, j = blockIdx.x * 128 + tid;
     const int id = ids[t];
     const bool none = id < 0 || id >= n_adapters;
     const int64_t at = (int64_t)t * J + j;
+    const float scaled = none ? 0.f : scale[id];
     float s = 0.f;
     if (j < J && base) s = base[at];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1083,7 +1084,7 @@ __global__ void __launch_bounds__(128)
         for (int q = tid; q < r; q += 128) {
             float v = 0.f;
             for (int i = 0; i < slices; ++i) v += part[((int64_t)i * N + t) * r + q];
-            u[q] = v;
+            u[q] = v * scaled;  // the whole sum: parts that cancel may be past the range, scaled
         }
         __syncthreads();
         if (j < J) {
@@ -1385,7 +1386,7 @@ cudaError_t forward(const moe_adapter_params& p, const T* x, const T* W, const T
     if (few) {
         const int slice = ((p.d_in + slices - 1) / slices + 7) / 8 * 8;
         adapter_few_shrink_kernel<T><<<dim3(slices, (unsigned)p.N), 128, 0, st>>>(
-            x, A, scale, ids, (int)p.N, p.d_in, p.r, p.n_adapters, slice, part, plan.counters);
+            x, A, ids, (int)p.N, p.d_in, p.r, p.n_adapters, slice, part, plan.counters);
         e = cudaGetLastError();
     } else {
         e = launch_plan(p, ids, plan, st);
@@ -1414,8 +1415,8 @@ cudaError_t forward(const moe_adapter_params& p, const T* x, const T* W, const T
     }
     if (!few) return launch_expand<T, false>(p, u, B, p.d_out, base, y, W != nullptr, plan, st);
     return launch(adapter_few_expand_kernel<T>, dim3((unsigned)((p.d_out + 127) / 128), (unsigned)p.N), 128, 0, st, !W,
-                  (const float*)part, slices, B, ids, (int)p.N, p.d_out, p.r, p.n_adapters, base, y, (int)(W != nullptr),
-                  plan.counters);
+                  (const float*)part, slices, B, scale, ids, (int)p.N, p.d_out, p.r, p.n_adapters, base, y,
+                  (int)(W != nullptr), plan.counters);
 }
 
 template <typename T>
